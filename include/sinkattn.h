@@ -53,14 +53,16 @@ typedef enum sa_status {
   SA_ERR_STALE_SNAPSHOT = 5,   /* restore after rows below the snapshot were rewritten */
   SA_ERR_CUDA = 6,             /* a CUDA runtime/driver call failed (launch, tensor map) */
   SA_ERR_TIMEOUT = 7,          /* a bounded device wait ran out (read via sa_get_device_status) */
-  SA_ERR_WORKSPACE = 8,        /* decode workspace missing or too small */
-  SA_ERR_UNSUPPORTED = 9       /* operation not provided for this cache format (prefill on FP8) */
+  SA_ERR_WORKSPACE = 8,        /* workspace missing or too small */
+  SA_ERR_UNSUPPORTED = 9       /* operation not provided for this cache format (sa_attn_prefill on
+                                  FP8 or INT4, sa_attn_prefill_quant on bf16) */
 } sa_status;
 
 /* Element format of a cache (sa_kv_cache.kv_dtype). */
 typedef enum sa_kv_dtype {
   SA_KV_BF16 = 0,      /* bf16 rows */
-  SA_KV_FP8_E4M3 = 1   /* e4m3 codes + one fp32 scale per row (sa_kv_cache_init_fp8) */
+  SA_KV_FP8_E4M3 = 1,  /* e4m3 codes + one fp32 scale per row (sa_kv_cache_init_fp8) */
+  SA_KV_INT4 = 2       /* 4-bit codes + one bf16 scale per 32 elements (sa_kv_cache_init_int4) */
 } sa_kv_dtype;
 
 /* Capacity of the cache's overwrite log (see sa_kv_restore). */
@@ -90,9 +92,13 @@ typedef enum sa_kv_dtype {
  * kv_dtype, k_scale, v_scale: SA_KV_BF16 with NULL scales, or
  *        SA_KV_FP8_E4M3: k and v then hold e4m3 codes (one byte per element,
  *        same [B][n_kv][cap][d] layout) and k_scale / v_scale fp32
- *        [B][n_kv][cap] row scales (see sa_kv_cache_init_fp8).
+ *        [B][n_kv][cap] row scales (see sa_kv_cache_init_fp8), or
+ *        SA_KV_INT4: k and v hold two codes per byte ([B][n_kv][cap][d/2]) and
+ *        k_scale / v_scale bf16 [B][n_kv][cap][d/32] block scales (see
+ *        sa_kv_cache_init_int4).
  * The remaining fields are bookkeeping for snapshot/restore; initialise the
- * whole struct with sa_kv_cache_init (or _ring, _fp8) and do not edit them.
+ * whole struct with sa_kv_cache_init (or _ring, _fp8, _int4) and do not edit
+ * them.
  */
 typedef struct sa_kv_cache {
   void* k;
@@ -108,7 +114,7 @@ typedef struct sa_kv_cache {
   int64_t log_floor_row; /* latest dropped seq, lowest dropped row        */
   int32_t ring;          /* 0: linear; > 0: ring cache for `ring`-key bands */
   int32_t kv_dtype;      /* sa_kv_dtype */
-  void* k_scale;         /* FP8 only: fp32 [B][n_kv][cap] */
+  void* k_scale;         /* FP8: fp32 [B][n_kv][cap]; INT4: bf16 [B][n_kv][cap][d/32] */
   void* v_scale;
 } sa_kv_cache;
 
@@ -222,21 +228,60 @@ sa_status sa_kv_cache_init_ring(sa_kv_cache* cache, void* k, void* v, int32_t B,
  * sa_attn_decode, which also attends its quantised value) quantise;
  * sa_attn_prefill returns SA_ERR_UNSUPPORTED on an FP8 cache: run prefill
  * on a bf16 cache and move its rows over with sa_kv_append (strides
- * {n_kv*cap*d, d, cap*d} describe a bf16 cache as [B][T][n_kv][d]).
+ * {n_kv*cap*d, d, cap*d} describe a bf16 cache as [B][T][n_kv][d]), or call
+ * sa_attn_prefill_quant.
  * Buffers of a ring cache, scales included, must be zeroed before first use.
  */
 sa_status sa_kv_cache_init_fp8(sa_kv_cache* cache, void* k, void* v, void* k_scale, void* v_scale,
                                int32_t B, int32_t cap, int32_t n_kv, int32_t d, int32_t window);
 
 /*
+ * INT4 cache: 4.5 bits an element, for long contexts whose decode is bound by
+ * the bytes of the cache (MoE-Xtend README, "ROADMAP", as above): a row of
+ * d elements takes d/2 + d/16 bytes instead of 2 d.
+ * k, v    : device codes [B][n_kv][cap][d/2], 16-byte aligned: element 2i of
+ *           a row in the low half of byte i, element 2i+1 in the high half.
+ * k_scale, v_scale: device bf16 [B][n_kv][cap][d/32], 16-byte aligned.
+ * window  : as for sa_kv_cache_init_fp8; cap a multiple of 16 (SA_ERR_SHAPE).
+ * Each block of 32 elements x of a stored row (the bf16 row a bf16 cache
+ * would hold), with m its element of largest magnitude (of m and -m the
+ * positive one), is kept as
+ *   scale s = -m/8 rounded to 5 significant bits (nearest, ties to even),
+ *   codes u = min(15, floor(x/s + 8.5)),
+ * and every reader sees s*(u-8), which is exactly a bf16 number: the error is
+ * at most |m|/15 for |x| <= 7/8 |m| or x of m's sign, and at most |m|/6
+ * otherwise. Rows read back (sa_kv_read) and appended to an INT4 cache again
+ * give the same codes. A block whose m is under 2^-120 is kept as zeros; a
+ * block that holds an infinity or a NaN reads as 32 NaNs. Values of V beyond
+ * 2^100 may overflow the sums of sa_attn_decode.
+ * Buffers of a ring cache, scales included, must be zeroed before first use.
+ */
+sa_status sa_kv_cache_init_int4(sa_kv_cache* cache, void* k, void* v, void* k_scale, void* v_scale,
+                                int32_t B, int32_t cap, int32_t n_kv, int32_t d, int32_t window);
+
+/*
  * Append T already-rotated K rows and V rows at [offset, offset+T), then
  * offset += T (MoE-Xtend README, "KV CACHE": Cache.extend). k_rot/v: device
  * bf16 [B][T][n_kv][d] via strides. Bit copy into a bf16 cache; into an FP8
- * cache each row is quantised (sa_kv_cache_init_fp8). SA_ERR_CAPACITY if
- * offset + T > cap.
+ * or INT4 cache each row is quantised (sa_kv_cache_init_fp8, _int4).
+ * SA_ERR_CAPACITY if offset + T > cap.
  */
 sa_status sa_kv_append(sa_kv_cache* cache, const void* k_rot, const int64_t k_strides[3],
                        const void* v, const int64_t v_strides[3], int32_t T, sa_stream_t stream);
+
+/*
+ * Read positions [start, start+T) back as bf16 rows, of a cache of any format
+ * (to go on in bf16 after a quantised decode, to move rows between caches of
+ * different formats or capacities, to look at them). k_out, v_out: device
+ * bf16 [B][T][n_kv][d] via strides, which must not overlap the cache; K rows
+ * are the rotated ones. bf16 rows are copied; FP8 rows are code * scale
+ * rounded to bf16 once; INT4 rows are exact. The cache is not changed.
+ * SA_ERR_CAPACITY unless the cache holds all of the positions: start + T <=
+ * offset, and for a ring start >= (the largest offset reached) - cap.
+ * T == 0 is a no-op.
+ */
+sa_status sa_kv_read(const sa_kv_cache* cache, int64_t start, int32_t T, void* k_out, const int64_t k_strides[3],
+                     void* v_out, const int64_t v_strides[3], sa_stream_t stream);
 
 /* Capture the cache state (offset; rows below it are immutable under
  * append-only use). Host only, no device work. */
@@ -281,9 +326,32 @@ sa_status sa_kv_restore(sa_kv_cache* cache, const sa_snapshot* snap);
  * take a second kernel instead: the staging launch only
  * appends K/V, the kernel reads q directly and rotates it itself, no
  * schedule counter is used, and `out` may again be `q` itself.
- * SA_ERR_UNSUPPORTED on an FP8 cache.
+ * SA_ERR_UNSUPPORTED on an FP8 or INT4 cache (sa_attn_prefill_quant).
  */
 sa_status sa_attn_prefill(sa_kv_cache* cache, const sa_attn_args* args, sa_stream_t stream);
+
+/*
+ * Prefill on an FP8 or INT4 cache: the next turn of a conversation whose
+ * cache is quantised. Arguments, masks, sinks and errors as sa_attn_prefill;
+ * the call's K rows are rotated (if rope_fused), all T rows are quantised
+ * into the cache, and the queries attend every row, the call's own included,
+ * as sa_kv_read returns it. cache->offset += T on success.
+ * workspace: device memory of sa_attn_prefill_quant_workspace_size() bytes,
+ *   16-byte aligned, contents irrelevant: the rows that the call attends as
+ *   bf16 (reading them back once costs a fraction of the attention over them
+ *   for all heads and rows). Calls that share a workspace must not overlap on
+ *   the device; it may be shared by all layers of a model.
+ * `out` may be `q` itself but must not overlap the workspace otherwise.
+ * Schedule counters and graph capture as for sa_attn_prefill.
+ * SA_ERR_UNSUPPORTED on a bf16 cache (sa_attn_prefill); SA_ERR_WORKSPACE.
+ */
+sa_status sa_attn_prefill_quant(sa_kv_cache* cache, const sa_attn_args* args, void* workspace, size_t workspace_bytes,
+                                sa_stream_t stream);
+
+/* Workspace bytes of sa_attn_prefill_quant for T rows at the cache's present
+ * offset: K and V of T + (window > 0 ? min(offset, window - 1) : offset)
+ * positions in bf16. 0 for an invalid cache or T < 1. */
+size_t sa_attn_prefill_quant_workspace_size(const sa_kv_cache* cache, int32_t T, int32_t window);
 
 /*
  * Decode: one new row per sequence (args->T must be 1). Rotates q and k,
@@ -294,7 +362,10 @@ sa_status sa_attn_prefill(sa_kv_cache* cache, const sa_attn_args* args, sa_strea
  * kernel dequantises K/V as it reads them and stores and attends the new
  * row quantised; queries enter the QK product as f16 after an exact
  * per-head power-of-two scaling, and the scaled softmax weights enter the PV
- * product as f16.
+ * product as f16. On an INT4 cache the new row is likewise stored and
+ * attended quantised; codes enter both products as integers, queries the QK
+ * product in f16 after an exact per-head power-of-two scaling, the weights
+ * times the block scales of V the PV product as bf16.
  * The rows are shared out among the CTAs of each (sequence, KV head) at run
  * time (the CTAs that stream faster take more), so the fp32 partial sums are
  * grouped differently from call to call: two identical calls can differ in

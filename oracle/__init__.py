@@ -31,10 +31,13 @@ Modules, each citing the passage it restates:
                    dequantise (MoE-Xtend README, "ROADMAP": KV quantisation
                    with dequantisation; the format is a reading, pinned by
                    ``tests/test_oracle_fp8.py``).
+* ``int4``      -- 4-bit rows with one bf16 scale per 32 elements: quantise
+                   and dequantise (same source; the format is this library's
+                   own, pinned by ``tests/test_oracle_int4.py``).
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``
 except the two readings listed there as "parity unpinned" (the RoPE pair
 convention against a real checkpoint, and the GPT-OSS-Lite rotary base).
 """
 
-from . import bf16, yarn, rope, attention, kvcache, fp8, linear, backward  # noqa: F401
+from . import bf16, yarn, rope, attention, kvcache, fp8, int4, linear, backward  # noqa: F401

@@ -14,10 +14,12 @@ from .sinkattn import (  # noqa: F401
     attn_decode,
     attn_decode_static,
     attn_prefill,
+    attn_prefill_quant,
     decode_workspace,
     decode_workspace_bytes,
     device_status,
     out_proj,
+    prefill_quant_workspace,
     qkv_proj,
     rmsnorm_fold_weight,
     rope_apply_qk,

@@ -452,6 +452,167 @@ __device__ __forceinline__ void load_q_words(const __nv_bfloat16* qrow, int lane
   }
 }
 
+// The end of a decode CTA's work, shared by the decode kernels: merges the
+// consumer warps' partials in shared memory ([NCW][8 m | 8 l | 8*D O] fp32 at
+// C::OFF_RED) and, with S > 1, the splits' records. Called by the 32 * NCW
+// consumer threads, after a barrier behind the partials' stores.
+template <int D, typename C>
+__device__ __forceinline__ void decode_finish(const DecodeParams& p, uint8_t* smem, uint32_t sbase,
+                                              uint32_t merge_bar, volatile int* flag, const float* sink_sm, int g,
+                                              int split, int b) {
+  const int QM = p.q_mult;
+  const float* red = reinterpret_cast<const float*>(smem + C::OFF_RED);
+  const float LN2 = 0.6931471805599453f;
+  const int tid = threadIdx.x;  // 0 .. 32*NCW-1
+  constexpr int NT = 32 * C::NCW;
+  const int RF = p.rec_floats;
+  float* rec = p.ws_rec + (((long long)b * p.n_kv + g) * p.S + split) * RF;
+  // two adjacent outputs (head n, dims d, d+1) per thread and pass
+  for (int idx = 2 * tid; idx < QM * D; idx += 2 * NT) {
+    const int n = idx / D, d = idx % D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < C::NCW; ++w) M = fmaxf(M, red[w * (C::RED_WARP / 4) + n]);
+    const float Mu = (M == -INFINITY) ? 0.f : M;
+    float L = 0.f, O0 = 0.f, O1 = 0.f;
+#pragma unroll
+    for (int w = 0; w < C::NCW; ++w) {
+      const float* rw = red + w * (C::RED_WARP / 4);
+      const float f = ex2(rw[n] - Mu);
+      L += rw[8 + n] * f;
+      const float2 ov = *reinterpret_cast<const float2*>(rw + 16 + n * D + d);
+      O0 += ov.x * f;
+      O1 += ov.y * f;
+    }
+    const int h = g * QM + n;
+    if (p.S == 1) {
+      const float sink2 = sink_sm[n];
+      const float M2 = fmaxf(M, sink2);
+      const float fo = ex2(M - M2);
+      const float tot = L * fo + ex2(sink2 - M2);
+      *reinterpret_cast<uint32_t*>(p.out + b * p.os0 + (long long)h * p.os2 + d) =
+          pack_bf16(O0 * fo / tot, O1 * fo / tot);
+      if (d == 0 && p.lse) p.lse[(long long)b * p.n_q + h] = (M2 + __log2f(tot)) * LN2;
+    } else {
+      *reinterpret_cast<float2*>(rec + n * D + d) = make_float2(O0, O1);
+      if (d == 0) {
+        rec[QM * D + n] = M;
+        rec[QM * D + QM + n] = L;
+      }
+    }
+  }
+  if (p.S == 1) return;
+
+  // The ticket: the barrier orders every thread's record stores before
+  // thread 0's release; its acquire makes the other CTAs' records visible to
+  // the merging CTA (whose thread 0 alone reads them, by bulk copy).
+  named_bar_sync(1, NT);
+  if (tid == 0) {
+    const int ticket = atom_add_acq_rel_gpu(p.ws_cnt + (b * p.n_kv + g), 1);
+    flag[1] = (ticket == p.S - 1) ? 1 : 0;
+  }
+  named_bar_sync(1, NT);
+  if (!flag[1]) return;
+
+  // Merge the S records of (b, g). The K/V ring is idle now: one bulk copy
+  // per round brings as many records as it holds (normally all S) into it,
+  // so the tail pays one memory round trip instead of one per batch of
+  // loads. A group of G adjacent lanes owns four outputs (head n, dims
+  // d .. d+3); its lanes take every G-th record and combine by shuffles.
+  // The running maximum starts at the sink (log2 units):
+  // M = max(sink, m_s), l = e^{sink-M} + sum_s e^{m_s-M} l_s.
+  const int S = p.S;
+  const uint32_t rec_bytes = (uint32_t)RF * 4u;
+  const int per_round = (int)(C::RING_BYTES / rec_bytes);
+  const float* recs = reinterpret_cast<const float*>(smem);
+  const char* gsrc = reinterpret_cast<const char*>(p.ws_rec + ((long long)b * p.n_kv + g) * S * RF);
+  const int nf4 = QM * D / 4;
+  const int G = 2 * nf4 <= NT ? 2 : 1;   // lanes per output group
+  const int f4 = tid / G, part = tid % G;
+  const bool owner = f4 < nf4;
+  const int n = owner ? (4 * f4) / D : 0;
+  const int d = owner ? (4 * f4) % D : 0;
+  const int om = QM * D + n, ol = QM * D + QM + n, oo = n * D + d;
+  float M = sink_sm[n];
+  float L = (M == -INFINITY) ? 0.f : 1.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0, r = 0; s0 < S; s0 += per_round, ++r) {
+    const int cnt = S - s0 < per_round ? S - s0 : per_round;
+    if (tid == 0) {
+      // the records were written by generic stores (other CTAs', acquired
+      // through the ticket) and the ring was last written the same way
+      fence_proxy_async_global();
+      fence_proxy_async_smem();
+      const uint32_t bytes = (uint32_t)cnt * rec_bytes;
+      mbar_arrive_expect_tx(merge_bar, bytes);
+      for (uint32_t o = 0; o < bytes; o += 32768u)
+        bulk_load(sbase + o, gsrc + (size_t)s0 * rec_bytes + o, bytes - o < 32768u ? bytes - o : 32768u,
+                  merge_bar);
+    }
+    // a wait that runs out is recorded in the status word; the copy is then
+    // drained before the ring is read or this CTA exits
+    if (!mbar_wait(merge_bar, (uint32_t)(r & 1))) mbar_wait_drain(merge_bar, (uint32_t)(r & 1));
+    float Mr = M;
+    float4 ar = make_float4(0.f, 0.f, 0.f, 0.f);
+    float Lr = 0.f;
+    if (owner) {
+      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+      int s2 = part;
+      for (; s2 + 3 * G < cnt; s2 += 4 * G) {
+        m0 = fmaxf(m0, recs[s2 * RF + om]);
+        m1 = fmaxf(m1, recs[(s2 + G) * RF + om]);
+        m2 = fmaxf(m2, recs[(s2 + 2 * G) * RF + om]);
+        m3 = fmaxf(m3, recs[(s2 + 3 * G) * RF + om]);
+      }
+      for (; s2 < cnt; s2 += G) m0 = fmaxf(m0, recs[s2 * RF + om]);
+      Mr = fmaxf(fmaxf(Mr, fmaxf(m0, m1)), fmaxf(m2, m3));
+    }
+    if (G == 2) Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 1));
+    const float Mu = (Mr == -INFINITY) ? 0.f : Mr;
+    if (owner) {
+#pragma unroll 4
+      for (int s2 = part; s2 < cnt; s2 += G) {
+        const float* rr = recs + s2 * RF;
+        const float w = ex2(rr[om] - Mu);
+        Lr = fmaf(w, rr[ol], Lr);
+        const float4 v = *reinterpret_cast<const float4*>(rr + oo);
+        ar.x = fmaf(w, v.x, ar.x);
+        ar.y = fmaf(w, v.y, ar.y);
+        ar.z = fmaf(w, v.z, ar.z);
+        ar.w = fmaf(w, v.w, ar.w);
+      }
+    }
+    if (G == 2) {
+      Lr += __shfl_xor_sync(0xffffffffu, Lr, 1);
+      ar.x += __shfl_xor_sync(0xffffffffu, ar.x, 1);
+      ar.y += __shfl_xor_sync(0xffffffffu, ar.y, 1);
+      ar.z += __shfl_xor_sync(0xffffffffu, ar.z, 1);
+      ar.w += __shfl_xor_sync(0xffffffffu, ar.w, 1);
+    }
+    const float f = ex2(M - Mu);
+    L = fmaf(L, f, Lr);
+    acc.x = fmaf(acc.x, f, ar.x);
+    acc.y = fmaf(acc.y, f, ar.y);
+    acc.z = fmaf(acc.z, f, ar.z);
+    acc.w = fmaf(acc.w, f, ar.w);
+    M = Mr;
+    named_bar_sync(1, NT);   // the ring is read before the next round's copy overwrites it
+  }
+  if (owner && part == 0) {
+    const int h = g * QM + n;
+    const float inv = 1.0f / L;
+    uint2 packed;
+    packed.x = pack_bf16(acc.x * inv, acc.y * inv);
+    packed.y = pack_bf16(acc.z * inv, acc.w * inv);
+    *reinterpret_cast<uint2*>(p.out + b * p.os0 + (long long)h * p.os2 + d) = packed;
+    if (d == 0 && p.lse) p.lse[(long long)b * p.n_q + h] = (M + __log2f(L)) * LN2;
+  }
+  if (tid == 0) {
+    p.ws_cnt[b * p.n_kv + g] = 0;
+    p.ws_grab[b * p.n_kv + g] = 0;
+  }
+}
+
 // tmK/tmV: the cache's K/V (bf16 elements, or FP8 code bytes); tmKS/tmVS
 // (FP8 only): the row scales, dims {rows, n_kv, B, 1}, box {R, 1, 1, 1}.
 template <int D, bool F8>
@@ -883,155 +1044,7 @@ __global__ void __launch_bounds__(288, 2)
   }
   named_bar_sync(1, 32 * C::NCW);
 
-  const float LN2 = 0.6931471805599453f;
-  const int tid = threadIdx.x;  // 0 .. 32*NCW-1
-  constexpr int NT = 32 * C::NCW;
-  const int RF = p.rec_floats;
-  float* rec = p.ws_rec + (((long long)b * p.n_kv + g) * p.S + split) * RF;
-  // two adjacent outputs (head n, dims d, d+1) per thread and pass
-  for (int idx = 2 * tid; idx < QM * D; idx += 2 * NT) {
-    const int n = idx / D, d = idx % D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < C::NCW; ++w) M = fmaxf(M, red[w * (C::RED_WARP / 4) + n]);
-    const float Mu = (M == -INFINITY) ? 0.f : M;
-    float L = 0.f, O0 = 0.f, O1 = 0.f;
-#pragma unroll
-    for (int w = 0; w < C::NCW; ++w) {
-      const float* rw = red + w * (C::RED_WARP / 4);
-      const float f = ex2(rw[n] - Mu);
-      L += rw[8 + n] * f;
-      const float2 ov = *reinterpret_cast<const float2*>(rw + 16 + n * D + d);
-      O0 += ov.x * f;
-      O1 += ov.y * f;
-    }
-    const int h = g * QM + n;
-    if (p.S == 1) {
-      const float sink2 = sink_sm[n];
-      const float M2 = fmaxf(M, sink2);
-      const float fo = ex2(M - M2);
-      const float tot = L * fo + ex2(sink2 - M2);
-      *reinterpret_cast<uint32_t*>(p.out + b * p.os0 + (long long)h * p.os2 + d) =
-          pack_bf16(O0 * fo / tot, O1 * fo / tot);
-      if (d == 0 && p.lse) p.lse[(long long)b * p.n_q + h] = (M2 + __log2f(tot)) * LN2;
-    } else {
-      *reinterpret_cast<float2*>(rec + n * D + d) = make_float2(O0, O1);
-      if (d == 0) {
-        rec[QM * D + n] = M;
-        rec[QM * D + QM + n] = L;
-      }
-    }
-  }
-  if (p.S == 1) return;
-
-  // The ticket: the barrier orders every thread's record stores before
-  // thread 0's release; its acquire makes the other CTAs' records visible to
-  // the merging CTA (whose thread 0 alone reads them, by bulk copy).
-  named_bar_sync(1, NT);
-  if (tid == 0) {
-    const int ticket = atom_add_acq_rel_gpu(p.ws_cnt + (b * p.n_kv + g), 1);
-    flag[1] = (ticket == p.S - 1) ? 1 : 0;
-  }
-  named_bar_sync(1, NT);
-  if (!flag[1]) return;
-
-  // Merge the S records of (b, g). The K/V ring is idle now: one bulk copy
-  // per round brings as many records as it holds (normally all S) into it,
-  // so the tail pays one memory round trip instead of one per batch of
-  // loads. A group of G adjacent lanes owns four outputs (head n, dims
-  // d .. d+3); its lanes take every G-th record and combine by shuffles.
-  // The running maximum starts at the sink (log2 units):
-  // M = max(sink, m_s), l = e^{sink-M} + sum_s e^{m_s-M} l_s.
-  const int S = p.S;
-  const uint32_t rec_bytes = (uint32_t)RF * 4u;
-  const int per_round = (int)(C::RING_BYTES / rec_bytes);
-  const float* recs = reinterpret_cast<const float*>(smem);
-  const char* gsrc = reinterpret_cast<const char*>(p.ws_rec + ((long long)b * p.n_kv + g) * S * RF);
-  const int nf4 = QM * D / 4;
-  const int G = 2 * nf4 <= NT ? 2 : 1;   // lanes per output group
-  const int f4 = tid / G, part = tid % G;
-  const bool owner = f4 < nf4;
-  const int n = owner ? (4 * f4) / D : 0;
-  const int d = owner ? (4 * f4) % D : 0;
-  const int om = QM * D + n, ol = QM * D + QM + n, oo = n * D + d;
-  float M = sink_sm[n];
-  float L = (M == -INFINITY) ? 0.f : 1.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0, r = 0; s0 < S; s0 += per_round, ++r) {
-    const int cnt = S - s0 < per_round ? S - s0 : per_round;
-    if (tid == 0) {
-      // the records were written by generic stores (other CTAs', acquired
-      // through the ticket) and the ring was last written the same way
-      fence_proxy_async_global();
-      fence_proxy_async_smem();
-      const uint32_t bytes = (uint32_t)cnt * rec_bytes;
-      mbar_arrive_expect_tx(merge_bar, bytes);
-      for (uint32_t o = 0; o < bytes; o += 32768u)
-        bulk_load(sbase + o, gsrc + (size_t)s0 * rec_bytes + o, bytes - o < 32768u ? bytes - o : 32768u,
-                  merge_bar);
-    }
-    // a wait that runs out is recorded in the status word; the copy is then
-    // drained before the ring is read or this CTA exits
-    if (!mbar_wait(merge_bar, (uint32_t)(r & 1))) mbar_wait_drain(merge_bar, (uint32_t)(r & 1));
-    float Mr = M;
-    float4 ar = make_float4(0.f, 0.f, 0.f, 0.f);
-    float Lr = 0.f;
-    if (owner) {
-      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-      int s2 = part;
-      for (; s2 + 3 * G < cnt; s2 += 4 * G) {
-        m0 = fmaxf(m0, recs[s2 * RF + om]);
-        m1 = fmaxf(m1, recs[(s2 + G) * RF + om]);
-        m2 = fmaxf(m2, recs[(s2 + 2 * G) * RF + om]);
-        m3 = fmaxf(m3, recs[(s2 + 3 * G) * RF + om]);
-      }
-      for (; s2 < cnt; s2 += G) m0 = fmaxf(m0, recs[s2 * RF + om]);
-      Mr = fmaxf(fmaxf(Mr, fmaxf(m0, m1)), fmaxf(m2, m3));
-    }
-    if (G == 2) Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 1));
-    const float Mu = (Mr == -INFINITY) ? 0.f : Mr;
-    if (owner) {
-#pragma unroll 4
-      for (int s2 = part; s2 < cnt; s2 += G) {
-        const float* rr = recs + s2 * RF;
-        const float w = ex2(rr[om] - Mu);
-        Lr = fmaf(w, rr[ol], Lr);
-        const float4 v = *reinterpret_cast<const float4*>(rr + oo);
-        ar.x = fmaf(w, v.x, ar.x);
-        ar.y = fmaf(w, v.y, ar.y);
-        ar.z = fmaf(w, v.z, ar.z);
-        ar.w = fmaf(w, v.w, ar.w);
-      }
-    }
-    if (G == 2) {
-      Lr += __shfl_xor_sync(0xffffffffu, Lr, 1);
-      ar.x += __shfl_xor_sync(0xffffffffu, ar.x, 1);
-      ar.y += __shfl_xor_sync(0xffffffffu, ar.y, 1);
-      ar.z += __shfl_xor_sync(0xffffffffu, ar.z, 1);
-      ar.w += __shfl_xor_sync(0xffffffffu, ar.w, 1);
-    }
-    const float f = ex2(M - Mu);
-    L = fmaf(L, f, Lr);
-    acc.x = fmaf(acc.x, f, ar.x);
-    acc.y = fmaf(acc.y, f, ar.y);
-    acc.z = fmaf(acc.z, f, ar.z);
-    acc.w = fmaf(acc.w, f, ar.w);
-    M = Mr;
-    named_bar_sync(1, NT);   // the ring is read before the next round's copy overwrites it
-  }
-  if (owner && part == 0) {
-    const int h = g * QM + n;
-    const float inv = 1.0f / L;
-    uint2 packed;
-    packed.x = pack_bf16(acc.x * inv, acc.y * inv);
-    packed.y = pack_bf16(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(p.out + b * p.os0 + (long long)h * p.os2 + d) = packed;
-    if (d == 0 && p.lse) p.lse[(long long)b * p.n_q + h] = (M + __log2f(L)) * LN2;
-  }
-  if (tid == 0) {
-    p.ws_cnt[b * p.n_kv + g] = 0;
-    p.ws_grab[b * p.n_kv + g] = 0;
-  }
+  decode_finish<D, C>(p, smem, sbase, merge_bar, flag, sink_sm, g, split, b);
 }
 
 }  // namespace sa

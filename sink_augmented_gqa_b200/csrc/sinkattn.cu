@@ -15,8 +15,10 @@
 #include "band.cuh"
 #include "backward_tc.cuh"
 #include "decode.cuh"
+#include "decode_int4.cuh"
 #include "fp8.cuh"
 #include "gemm.cuh"
+#include "int4.cuh"
 #include "prefill.cuh"
 #include "ptx.cuh"
 #include "rope.cuh"
@@ -120,6 +122,25 @@ bool make_codes_map(CUtensorMap* map, void* base, int d, int n_kv, long long row
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUtensorMapSwizzle sw = rowb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                 : (rowb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// INT4 caches: tensor map over the codes [B][n_kv][cap][d / 2] bytes exposing
+// rows [0, rows_valid), box {d / 2, 128, 1, 1}: 32- and 64-byte rows swizzled
+// over their width, 48-byte rows plain.
+bool make_i4_map(CUtensorMap* map, void* base, int d, int n_kv, long long rows_valid, int cap, int B) {
+  EncodeTiledFn enc = encode_fn();
+  if (enc == nullptr || rows_valid < 1) return false;
+  const int rowb = d / 2;
+  const cuuint64_t dims[4] = {(cuuint64_t)rowb, (cuuint64_t)rows_valid, (cuuint64_t)n_kv, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)rowb, (cuuint64_t)cap * rowb, (cuuint64_t)n_kv * cap * rowb};
+  const cuuint32_t box[4] = {(cuuint32_t)rowb, 128, 1, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUtensorMapSwizzle sw = rowb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                : (rowb == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_NONE);
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, estr,
                          CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -242,7 +263,7 @@ sa_status check_cache(const sa_kv_cache* c) {
   if (!head_dim_ok(c->d)) return SA_ERR_SHAPE;
   if (!aligned16(c->k) || !aligned16(c->v)) return SA_ERR_INVALID_ARG;
   if (c->ring < 0) return SA_ERR_INVALID_ARG;
-  if (c->kv_dtype == SA_KV_FP8_E4M3) {
+  if (c->kv_dtype == SA_KV_FP8_E4M3 || c->kv_dtype == SA_KV_INT4) {
     if (c->k_scale == nullptr || c->v_scale == nullptr || !aligned16(c->k_scale) || !aligned16(c->v_scale))
       return SA_ERR_INVALID_ARG;
     if (c->cap % 16 != 0) return SA_ERR_SHAPE;
@@ -538,8 +559,15 @@ size_t decode_ws_bytes(int B, int n_kv, int q_mult, int d, int S) {
   return decode_cnt_bytes(B, n_kv) + (size_t)B * n_kv * S * decode_rec_floats(q_mult, d) * 4;
 }
 
-// Cache rows per ring stage of decode_kernel<d, f8> (its Cfg::R).
-long long decode_stage_rows(int d, bool f8) {
+// Cache rows per ring stage of decode_kernel<d, f8> or decode_i4_kernel<d>
+// (its Cfg::R).
+long long decode_stage_rows(int d, int kv_dtype) {
+  if (kv_dtype == SA_KV_INT4) {
+    static_assert(sa::DecodeI4Cfg<64>::R == 256 && sa::DecodeI4Cfg<96>::R == 256 && sa::DecodeI4Cfg<128>::R == 256,
+                  "one stage height for every head width");
+    return 256;
+  }
+  const bool f8 = kv_dtype == SA_KV_FP8_E4M3;
   switch (d) {
     case 64: return f8 ? sa::DecodeCfgT<64, true>::R : sa::DecodeCfgT<64, false>::R;
     case 96: return f8 ? sa::DecodeCfgT<96, true>::R : sa::DecodeCfgT<96, false>::R;
@@ -549,20 +577,19 @@ long long decode_stage_rows(int d, bool f8) {
 
 // The rows one decode call reads and how they are split over CTAs: the
 // launch and the allocation-free entry point's size check both take it from
-// here. lo_mask: first admitted key; lo: first row streamed (ring and FP8
-// stages start on multiples of the stage height, so no TMA box wraps a ring
-// and the scale boxes start on their stage's first row).
+// here. lo_mask: first admitted key; lo: first row streamed (ring, FP8 and
+// INT4 stages start on multiples of the stage height, so no TMA box wraps a
+// ring and the scales start on their stage's first row).
 struct DecodePlan {
   long long lo_mask, lo;
   int S;   // CTAs per (b, g)
 };
 
 DecodePlan plan_decode(const sa_kv_cache* c, const sa_attn_args* a) {
-  const bool f8 = c->kv_dtype == SA_KV_FP8_E4M3;
-  const long long R = decode_stage_rows(c->d, f8);
+  const long long R = decode_stage_rows(c->d, c->kv_dtype);
   DecodePlan pl;
   pl.lo_mask = a->window > 0 ? (a->offset + 1 - a->window > 0 ? a->offset + 1 - a->window : 0) : 0;
-  pl.lo = (c->ring > 0 || f8) ? pl.lo_mask / R * R : pl.lo_mask;
+  pl.lo = (c->ring > 0 || c->kv_dtype != SA_KV_BF16) ? pl.lo_mask / R * R : pl.lo_mask;
   pl.S = decode_splits(a->B, c->n_kv, a->offset - pl.lo, R);
   return pl;
 }
@@ -571,12 +598,11 @@ DecodePlan plan_decode(const sa_kv_cache* c, const sa_attn_args* a) {
 // kernel ahead of it on the stream (rounded up to whole stages).
 constexpr long long kDecodePrefetchBytes = 128 * 1024;
 
-template <int D, bool F8>
-sa_status launch_decode(const sa_kv_cache* c, const sa_attn_args* a, void* ws, size_t ws_bytes,
-                        cudaStream_t stream) {
-  using Cfg = sa::DecodeCfgT<D, F8>;
+// The kernel parameters that every decode launch shares, for stages of R rows
+// that bring stage_tx bytes; SA_ERR_WORKSPACE when the split does not fit ws.
+sa_status fill_decode(DecodeParams& p, const sa_kv_cache* c, const sa_attn_args* a, long long R, uint32_t stage_tx,
+                      void* ws, size_t ws_bytes) {
   const int q_mult = a->n_q / c->n_kv;
-  DecodeParams p;
   p.off = a->offset;
   p.ring_cap = c->ring > 0 ? c->cap : 0;
   const DecodePlan pl = plan_decode(c, a);
@@ -584,35 +610,14 @@ sa_status launch_decode(const sa_kv_cache* c, const sa_attn_args* a, void* ws, s
   p.lo = pl.lo;
   const long long n_cache = p.off - p.lo;
   p.S = pl.S;
-  p.n_blocks = n_cache > 0 ? (n_cache + Cfg::R - 1) / Cfg::R : 0;
+  p.n_blocks = n_cache > 0 ? (n_cache + R - 1) / R : 0;
   // a lone CTA streams everything in order; with several, half of each
   // one's share is static and the rest dynamic
   p.static_stages = p.S == 1 ? (int)p.n_blocks : (int)(p.n_blocks / (2 * p.S));
-  p.pf_stages = (int)((kDecodePrefetchBytes + Cfg::STAGE_TX - 1) / Cfg::STAGE_TX);
+  p.pf_stages = (int)((kDecodePrefetchBytes + stage_tx - 1) / stage_tx);
   if (p.S > 1) {
-    if (ws == nullptr || !aligned16(ws) || ws_bytes < decode_ws_bytes(a->B, c->n_kv, q_mult, D, p.S))
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < decode_ws_bytes(a->B, c->n_kv, q_mult, c->d, p.S))
       return SA_ERR_WORKSPACE;
-  }
-  CUtensorMap tmK, tmV, tmKS, tmVS;
-  memset(&tmK, 0, sizeof(tmK));
-  memset(&tmV, 0, sizeof(tmV));
-  memset(&tmKS, 0, sizeof(tmKS));
-  memset(&tmVS, 0, sizeof(tmVS));
-  if (n_cache > 0) {
-    const long long rows = p.ring_cap > 0 ? (long long)c->cap : p.off;
-    constexpr int kBoxRows = Cfg::R / Cfg::NBOX;   // a stage is NBOX boxes of 128 rows
-    static_assert(kBoxRows == 128, "decode TMA boxes are 128 rows");
-    if constexpr (F8) {
-      if (!make_codes_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, kBoxRows, Cfg::ROWB) ||
-          !make_codes_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B, kBoxRows, Cfg::ROWB) ||
-          !make_scales_map(&tmKS, c->k_scale, c->n_kv, rows, c->cap, c->B, kBoxRows) ||
-          !make_scales_map(&tmVS, c->v_scale, c->n_kv, rows, c->cap, c->B, kBoxRows))
-        return SA_ERR_CUDA;
-    } else {
-      if (!make_cache_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, kBoxRows, Cfg::CB) ||
-          !make_cache_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B, kBoxRows, Cfg::CB))
-        return SA_ERR_CUDA;
-    }
   }
   p.q = static_cast<const __nv_bfloat16*>(a->q);
   p.qs0 = a->q_strides[0];
@@ -645,32 +650,158 @@ sa_status launch_decode(const sa_kv_cache* c, const sa_attn_args* a, void* ws, s
   p.ws_cnt = reinterpret_cast<int*>(w);
   p.ws_grab = p.ws_cnt + (size_t)a->B * c->n_kv;
   p.ws_rec = reinterpret_cast<float*>(w + decode_cnt_bytes(a->B, c->n_kv));
-  p.rec_floats = decode_rec_floats(q_mult, D);
-  static std::atomic<uint64_t> smem_set{0};
-  {
-    const sa_status sm = set_smem_once(sa::decode_kernel<D, F8>, Cfg::SMEM_BYTES, smem_set);
-    if (sm != SA_OK) return sm;
-  }
-  // Programmatic stream serialization: back-to-back decode launches (one per
-  // layer) overlap one kernel's drain with the next one's launch and set-up;
-  // the kernel waits for its predecessor before touching global memory.
+  p.rec_floats = decode_rec_floats(q_mult, c->d);
+  return SA_OK;
+}
+
+// Launches a decode kernel: grid n_kv x S x B, with programmatic stream
+// serialization: back-to-back decode launches (one per layer) overlap one
+// kernel's drain with the next one's launch and set-up; the kernel waits for
+// its predecessor before touching global memory.
+template <typename K, typename... A>
+sa_status launch_decode_kernel(K kernel, const sa_kv_cache* c, const DecodeParams& p, int threads, uint32_t smem,
+                               std::atomic<uint64_t>& smem_set, cudaStream_t stream, const A&... args) {
+  const sa_status sm = set_smem_once(kernel, smem, smem_set);
+  if (sm != SA_OK) return sm;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(c->n_kv, p.S, a->B);
-  lc.blockDim = dim3(Cfg::NUM_THREADS);
-  lc.dynamicSmemBytes = Cfg::SMEM_BYTES;
+  lc.gridDim = dim3(c->n_kv, p.S, p.B);
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, sa::decode_kernel<D, F8>, tmK, tmV, tmKS, tmVS, p);
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, args..., p);
   return (last_launch_status() == SA_OK && e == cudaSuccess) ? SA_OK : SA_ERR_CUDA;
+}
+
+template <int D, bool F8>
+sa_status launch_decode(const sa_kv_cache* c, const sa_attn_args* a, void* ws, size_t ws_bytes,
+                        cudaStream_t stream) {
+  using Cfg = sa::DecodeCfgT<D, F8>;
+  DecodeParams p;
+  const sa_status st = fill_decode(p, c, a, Cfg::R, Cfg::STAGE_TX, ws, ws_bytes);
+  if (st != SA_OK) return st;
+  CUtensorMap tmK, tmV, tmKS, tmVS;
+  memset(&tmK, 0, sizeof(tmK));
+  memset(&tmV, 0, sizeof(tmV));
+  memset(&tmKS, 0, sizeof(tmKS));
+  memset(&tmVS, 0, sizeof(tmVS));
+  if (p.n_blocks > 0) {
+    const long long rows = p.ring_cap > 0 ? (long long)c->cap : p.off;
+    constexpr int kBoxRows = Cfg::R / Cfg::NBOX;   // a stage is NBOX boxes of 128 rows
+    static_assert(kBoxRows == 128, "decode TMA boxes are 128 rows");
+    if constexpr (F8) {
+      if (!make_codes_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, kBoxRows, Cfg::ROWB) ||
+          !make_codes_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B, kBoxRows, Cfg::ROWB) ||
+          !make_scales_map(&tmKS, c->k_scale, c->n_kv, rows, c->cap, c->B, kBoxRows) ||
+          !make_scales_map(&tmVS, c->v_scale, c->n_kv, rows, c->cap, c->B, kBoxRows))
+        return SA_ERR_CUDA;
+    } else {
+      if (!make_cache_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, kBoxRows, Cfg::CB) ||
+          !make_cache_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B, kBoxRows, Cfg::CB))
+        return SA_ERR_CUDA;
+    }
+  }
+  static std::atomic<uint64_t> smem_set{0};
+  return launch_decode_kernel(sa::decode_kernel<D, F8>, c, p, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, smem_set, stream, tmK,
+                              tmV, tmKS, tmVS);
+}
+
+template <int D>
+sa_status launch_decode_i4(const sa_kv_cache* c, const sa_attn_args* a, void* ws, size_t ws_bytes,
+                           cudaStream_t stream) {
+  using Cfg = sa::DecodeI4Cfg<D>;
+  DecodeParams p;
+  const sa_status st = fill_decode(p, c, a, Cfg::R, Cfg::STAGE_TX, ws, ws_bytes);
+  if (st != SA_OK) return st;
+  CUtensorMap tmK, tmV;
+  memset(&tmK, 0, sizeof(tmK));
+  memset(&tmV, 0, sizeof(tmV));
+  if (p.n_blocks > 0) {
+    const long long rows = p.ring_cap > 0 ? (long long)c->cap : p.off;
+    if (!make_i4_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B) ||
+        !make_i4_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B))
+      return SA_ERR_CUDA;
+  }
+  static std::atomic<uint64_t> smem_set{0};
+  return launch_decode_kernel(sa::decode_i4_kernel<D>, c, p, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, smem_set, stream, tmK,
+                              tmV);
+}
+
+// A run of T bf16 rows beside cache rows from position pos on (int4.cuh).
+template <int D>
+sa::RowsParams rows_params(const sa_kv_cache* c, const void* k, const int64_t ks[3], const void* v,
+                           const int64_t vs[3], long long pos, int T) {
+  sa::RowsParams p;
+  p.ck = c->k;
+  p.cv = c->v;
+  p.cks = c->k_scale;
+  p.cvs = c->v_scale;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.ks0 = ks[0]; p.ks1 = ks[1]; p.ks2 = ks[2];
+  p.vs0 = vs[0]; p.vs1 = vs[1]; p.vs2 = vs[2];
+  p.T = T;
+  p.n_kv = c->n_kv;
+  p.cap = c->cap;
+  p.row0 = (int)(c->ring > 0 ? pos % c->cap : pos);
+  p.blocks_t = (T + sa::RowsCfg<D>::RB - 1) / sa::RowsCfg<D>::RB;
+  return p;
+}
+
+// Blocks of a row kernel; 0 when there are more than a grid holds.
+unsigned rows_grid(const sa_kv_cache* c, int blocks_t) {
+  const long long n = (long long)c->B * c->n_kv * blocks_t;
+  return n > INT32_MAX ? 0u : (unsigned)n;
+}
+
+template <int D>
+sa_status launch_append_i4(const sa_kv_cache* c, const void* k, const int64_t ks[3], const void* v,
+                           const int64_t vs[3], int T, cudaStream_t stream) {
+  const sa::RowsParams p = rows_params<D>(c, k, ks, v, vs, c->offset, T);
+  const unsigned grid = rows_grid(c, p.blocks_t);
+  if (grid == 0) return SA_ERR_SHAPE;
+  sa::kv_append_i4_kernel<D><<<grid, 256, 0, stream>>>(p);
+  return last_launch_status();
+}
+
+template <int D>
+sa_status launch_read(const sa_kv_cache* c, long long pos, void* k, const int64_t ks[3], void* v, const int64_t vs[3],
+                      int T, cudaStream_t stream) {
+  const sa::RowsParams p = rows_params<D>(c, k, ks, v, vs, pos, T);
+  const unsigned grid = rows_grid(c, p.blocks_t);
+  if (grid == 0) return SA_ERR_SHAPE;
+  switch (c->kv_dtype) {
+    case SA_KV_INT4: sa::kv_read_kernel<D, sa::ROWS_INT4><<<grid, 256, 0, stream>>>(p); break;
+    case SA_KV_FP8_E4M3: sa::kv_read_kernel<D, sa::ROWS_FP8><<<grid, 256, 0, stream>>>(p); break;
+    default: sa::kv_read_kernel<D, sa::ROWS_BF16><<<grid, 256, 0, stream>>>(p); break;
+  }
+  return last_launch_status();
+}
+
+sa_status launch_read(const sa_kv_cache* c, long long pos, void* k, const int64_t ks[3], void* v, const int64_t vs[3],
+                      int T, cudaStream_t stream) {
+  switch (c->d) {
+    case 64: return launch_read<64>(c, pos, k, ks, v, vs, T, stream);
+    case 96: return launch_read<96>(c, pos, k, ks, v, vs, T, stream);
+    default: return launch_read<128>(c, pos, k, ks, v, vs, T, stream);
+  }
 }
 
 sa_status launch_append(sa_kv_cache* c, const void* k, const int64_t ks[3], const void* v,
                         const int64_t vs[3], int T, int rope, const float* cos_t,
                         const float* sin_t, cudaStream_t stream) {
+  if (c->kv_dtype == SA_KV_INT4) {
+    if (rope) return SA_ERR_UNSUPPORTED;
+    switch (c->d) {
+      case 64: return launch_append_i4<64>(c, k, ks, v, vs, T, stream);
+      case 96: return launch_append_i4<96>(c, k, ks, v, vs, T, stream);
+      default: return launch_append_i4<128>(c, k, ks, v, vs, T, stream);
+    }
+  }
   if (c->kv_dtype == SA_KV_FP8_E4M3) {
     if (rope) return SA_ERR_UNSUPPORTED;
     const long long rows = (long long)c->B * T * c->n_kv;   // one warp per row
@@ -708,6 +839,50 @@ sa_status launch_stage(sa_kv_cache* c, const sa_attn_args* a, bool stage_q, cuda
       a->n_q, static_cast<__nv_bfloat16*>(a->out), a->out_strides[0], a->out_strides[1],
       a->out_strides[2], stage_q ? 1 : 0, c->ring > 0 ? 1 : 0);
   return last_launch_status();
+}
+
+// Prefill of the rows in a (T > 0) over bf16 cache c: stage(stage_q) puts the
+// call's K/V rows into c and, with stage_q, the rotated queries into a->out;
+// then the attention kernel.
+template <typename F>
+sa_status run_prefill(const sa_kv_cache* c, const sa_attn_args* a, cudaStream_t s, F&& stage) {
+  const cudaEvent_t ev0 = g_prefill_ev_before, ev1 = g_prefill_ev_after;
+  const int band_n = band_columns(c, a);
+  if (band_n > 0) {
+    // band layer with packed heads: the kernel rotates its own queries and
+    // needs no schedule slot
+    sa_status r = stage(false);
+    if (r != SA_OK) return r;
+    if (ev0 != nullptr && cudaEventRecord(ev0, s) != cudaSuccess) return SA_ERR_CUDA;
+    r = launch_band(c, a, band_n, s);
+    if (r == SA_OK && ev1 != nullptr && cudaEventRecord(ev1, s) != cudaSuccess) return SA_ERR_CUDA;
+    return r;
+  }
+  // The schedule slot (and the wait for its previous user) is taken before
+  // the staging launch, so nothing stands between the two kernels.
+  return with_sched_slot(s, [&](int slot) -> sa_status {
+    sa_status r = stage(a->rope_fused != 0);
+    if (r != SA_OK) return r;
+    if (ev0 != nullptr && cudaEventRecord(ev0, s) != cudaSuccess) return SA_ERR_CUDA;
+    switch (c->d) {
+      case 64: r = launch_prefill<64>(c, a, slot, s); break;
+      case 96: r = launch_prefill<96>(c, a, slot, s); break;
+      default: r = launch_prefill<128>(c, a, slot, s); break;
+    }
+    if (ev1 != nullptr && cudaEventRecord(ev1, s) != cudaSuccess) return SA_ERR_CUDA;
+    return r;
+  });
+}
+
+// Cached positions before the call's own that a prefill on cache c attends.
+long long quant_prefix(const sa_kv_cache* c, int window) {
+  return window > 0 && c->offset > window - 1 ? window - 1 : c->offset;
+}
+
+// Workspace of sa_attn_prefill_quant: bf16 K and V rows of those positions
+// and of the call's T.
+size_t quant_ws_bytes(const sa_kv_cache* c, int T, int window) {
+  return 2 * (size_t)c->B * c->n_kv * (size_t)(quant_prefix(c, window) + T) * c->d * 2;
 }
 
 // Scratch of sa_attn_decode_static: one fixed array per device, its device
@@ -937,6 +1112,18 @@ sa_status sa_kv_cache_init_fp8(sa_kv_cache* cache, void* k, void* v, void* k_sca
   return check_cache(cache);
 }
 
+sa_status sa_kv_cache_init_int4(sa_kv_cache* cache, void* k, void* v, void* k_scale, void* v_scale,
+                                int32_t B, int32_t cap, int32_t n_kv, int32_t d, int32_t window) {
+  if (cache == nullptr || window < 0) return SA_ERR_INVALID_ARG;
+  sa_status st = sa_kv_cache_init(cache, k, v, B, cap, n_kv, d);
+  if (st != SA_OK) return st;
+  cache->ring = window;
+  cache->kv_dtype = SA_KV_INT4;
+  cache->k_scale = k_scale;
+  cache->v_scale = v_scale;
+  return check_cache(cache);
+}
+
 sa_status sa_kv_append(sa_kv_cache* cache, const void* k_rot, const int64_t k_strides[3],
                        const void* v, const int64_t v_strides[3], int32_t T, sa_stream_t stream) {
   sa_status st = check_cache(cache);
@@ -954,6 +1141,21 @@ sa_status sa_kv_append(sa_kv_cache* cache, const void* k_rot, const int64_t k_st
   if (st != SA_OK) return st;
   note_append(cache, cache->offset, T);
   return SA_OK;
+}
+
+sa_status sa_kv_read(const sa_kv_cache* cache, int64_t start, int32_t T, void* k_out, const int64_t k_strides[3],
+                     void* v_out, const int64_t v_strides[3], sa_stream_t stream) {
+  sa_status st = check_cache(cache);
+  if (st != SA_OK) return st;
+  if (T < 0 || start < 0) return SA_ERR_INVALID_ARG;
+  // a ring holds the last cap positions written, of which those below offset count
+  const int64_t held = cache->ring > 0 && cache->high_water > cache->cap ? cache->high_water - cache->cap : 0;
+  if (start < held || start > cache->offset - T) return SA_ERR_CAPACITY;
+  if (T == 0) return SA_OK;
+  if (k_out == nullptr || v_out == nullptr || !aligned16(k_out) || !aligned16(v_out) || !strides_ok(k_strides) ||
+      !strides_ok(v_strides))
+    return SA_ERR_INVALID_ARG;
+  return launch_read(cache, start, k_out, k_strides, v_out, v_strides, T, (cudaStream_t)stream);
 }
 
 sa_status sa_kv_snapshot(const sa_kv_cache* cache, sa_snapshot* out) {
@@ -993,41 +1195,66 @@ sa_status sa_attn_prefill(sa_kv_cache* cache, const sa_attn_args* a, sa_stream_t
   if (a->T == 0) return SA_OK;
   cudaStream_t s = (cudaStream_t)stream;
   bool staged = false;
-  const int band_n = band_columns(cache, a);
-  if (band_n > 0) {
-    // band layer with packed heads: the staging launch appends K/V only (the
-    // kernel rotates its own queries) and the kernel needs no schedule slot
-    st = launch_stage(cache, a, false, s);
-    if (st == SA_OK) {
-      staged = true;
-      cudaEvent_t ev0 = g_prefill_ev_before, ev1 = g_prefill_ev_after;
-      if (ev0 != nullptr && cudaEventRecord(ev0, s) != cudaSuccess) st = SA_ERR_CUDA;
-      if (st == SA_OK) st = launch_band(cache, a, band_n, s);
-      if (st == SA_OK && ev1 != nullptr && cudaEventRecord(ev1, s) != cudaSuccess) st = SA_ERR_CUDA;
-    }
-    if (staged) note_append(cache, cache->offset, a->T);
-    return st;
-  }
-  // The schedule slot (and the wait for its previous user) is taken before
-  // the staging launch, so nothing stands between the two kernels.
-  st = with_sched_slot(s, [&](int slot) -> sa_status {
-    // one launch: the call's K rows rotated (when RoPE is fused) and appended
-    // with V, and the rotated queries staged in `out`
-    sa_status r = launch_stage(cache, a, a->rope_fused, s);
-    if (r != SA_OK) return r;
-    staged = true;
-    cudaEvent_t ev0 = g_prefill_ev_before, ev1 = g_prefill_ev_after;
-    if (ev0 != nullptr && cudaEventRecord(ev0, s) != cudaSuccess) return SA_ERR_CUDA;
-    switch (cache->d) {
-      case 64: r = launch_prefill<64>(cache, a, slot, s); break;
-      case 96: r = launch_prefill<96>(cache, a, slot, s); break;
-      default: r = launch_prefill<128>(cache, a, slot, s); break;
-    }
-    if (ev1 != nullptr && cudaEventRecord(ev1, s) != cudaSuccess) return SA_ERR_CUDA;
+  // one launch: the call's K rows rotated (when RoPE is fused) and appended
+  // with V, and (stage_q) the rotated queries staged in `out`
+  st = run_prefill(cache, a, s, [&](bool stage_q) -> sa_status {
+    const sa_status r = launch_stage(cache, a, stage_q, s);
+    staged = r == SA_OK;
     return r;
   });
   // Once the append is enqueued the offset follows it.
   if (staged) note_append(cache, cache->offset, a->T);
+  return st;
+}
+
+size_t sa_attn_prefill_quant_workspace_size(const sa_kv_cache* cache, int32_t T, int32_t window) {
+  if (check_cache(cache) != SA_OK || T < 1) return 0;
+  return quant_ws_bytes(cache, T, window);
+}
+
+sa_status sa_attn_prefill_quant(sa_kv_cache* cache, const sa_attn_args* a, void* workspace, size_t workspace_bytes,
+                                sa_stream_t stream) {
+  sa_status st = check_attn(cache, a);
+  if (st != SA_OK) return st;
+  if (cache->kv_dtype == SA_KV_BF16) return SA_ERR_UNSUPPORTED;
+  if (a->T == 0) return SA_OK;
+  if (workspace == nullptr || !aligned16(workspace) || workspace_bytes < quant_ws_bytes(cache, a->T, a->window))
+    return SA_ERR_WORKSPACE;
+  cudaStream_t s = (cudaStream_t)stream;
+  // The rows the call attends, positions [lo, off + T), as a bf16 cache in
+  // the workspace that starts at position lo: masks go by differences of
+  // positions, and the RoPE tables are passed from row lo on.
+  const long long prefix = quant_prefix(cache, a->window), lo = cache->offset - prefix;
+  const long long rows = prefix + a->T;
+  if (rows > INT32_MAX) return SA_ERR_CAPACITY;
+  sa_kv_cache w;
+  char* base = static_cast<char*>(workspace);
+  st = sa_kv_cache_init(&w, base, base + quant_ws_bytes(cache, a->T, a->window) / 2, cache->B, (int32_t)rows,
+                        cache->n_kv, cache->d);
+  if (st != SA_OK) return st;
+  w.offset = prefix;
+  sa_attn_args wa = *a;
+  wa.offset = prefix;
+  if (a->rope_fused) {
+    wa.cos = a->cos + lo * (cache->d / 2);
+    wa.sin = a->sin + lo * (cache->d / 2);
+    wa.max_pos = (int32_t)(a->max_pos - lo);
+  }
+  bool appended = false;
+  st = run_prefill(&w, &wa, s, [&](bool stage_q) -> sa_status {
+    // the call's rows, rotated, in the workspace; quantised from there into
+    // the cache; then all rows read back
+    sa_status r = launch_stage(&w, &wa, stage_q, s);
+    if (r != SA_OK) return r;
+    const int64_t ws[3] = {(int64_t)cache->n_kv * rows * cache->d, cache->d, rows * cache->d};
+    const long long row0 = prefix * cache->d;
+    __nv_bfloat16 *wk = static_cast<__nv_bfloat16*>(w.k), *wv = static_cast<__nv_bfloat16*>(w.v);
+    r = launch_append(cache, wk + row0, ws, wv + row0, ws, a->T, 0, nullptr, nullptr, s);
+    if (r != SA_OK) return r;
+    appended = true;
+    return launch_read(cache, lo, w.k, ws, w.v, ws, (int)rows, s);
+  });
+  if (appended) note_append(cache, cache->offset, a->T);
   return st;
 }
 
@@ -1038,19 +1265,22 @@ sa_status sa_attn_decode(sa_kv_cache* cache, const sa_attn_args* a, void* worksp
   if (a->T != 1) return SA_ERR_INVALID_ARG;
   if (a->n_q / cache->n_kv > 8) return SA_ERR_SHAPE;
   cudaStream_t s = (cudaStream_t)stream;
-  const bool f8 = cache->kv_dtype == SA_KV_FP8_E4M3;
+  const bool f8 = cache->kv_dtype == SA_KV_FP8_E4M3, i4 = cache->kv_dtype == SA_KV_INT4;
   switch (cache->d) {
     case 64:
-      st = f8 ? launch_decode<64, true>(cache, a, workspace, workspace_bytes, s)
-              : launch_decode<64, false>(cache, a, workspace, workspace_bytes, s);
+      st = i4 ? launch_decode_i4<64>(cache, a, workspace, workspace_bytes, s)
+           : f8 ? launch_decode<64, true>(cache, a, workspace, workspace_bytes, s)
+                : launch_decode<64, false>(cache, a, workspace, workspace_bytes, s);
       break;
     case 96:
-      st = f8 ? launch_decode<96, true>(cache, a, workspace, workspace_bytes, s)
-              : launch_decode<96, false>(cache, a, workspace, workspace_bytes, s);
+      st = i4 ? launch_decode_i4<96>(cache, a, workspace, workspace_bytes, s)
+           : f8 ? launch_decode<96, true>(cache, a, workspace, workspace_bytes, s)
+                : launch_decode<96, false>(cache, a, workspace, workspace_bytes, s);
       break;
     case 128:
-      st = f8 ? launch_decode<128, true>(cache, a, workspace, workspace_bytes, s)
-              : launch_decode<128, false>(cache, a, workspace, workspace_bytes, s);
+      st = i4 ? launch_decode_i4<128>(cache, a, workspace, workspace_bytes, s)
+           : f8 ? launch_decode<128, true>(cache, a, workspace, workspace_bytes, s)
+                : launch_decode<128, false>(cache, a, workspace, workspace_bytes, s);
       break;
     default: return SA_ERR_SHAPE;
   }

@@ -7,7 +7,8 @@ PyTorch fallback: if the library is missing, every call raises.
 
 Names mirror the C ABI in ``include/sinkattn.h`` without the ``sa_`` prefix:
 ``yarn_rope_tables``, ``rope_apply_qk``, ``KVCache`` (``kv_append``,
-``kv_snapshot``, ``kv_restore``), ``attn_prefill``, ``attn_decode``.
+``kv_read``, ``kv_snapshot``, ``kv_restore``), ``attn_prefill``,
+``attn_prefill_quant``, ``attn_decode``.
 """
 
 import ctypes
@@ -27,7 +28,7 @@ STATUS = {
     7: "SA_ERR_TIMEOUT", 8: "SA_ERR_WORKSPACE", 9: "SA_ERR_UNSUPPORTED",
 }
 
-KV_BF16, KV_FP8_E4M3 = 0, 1
+KV_BF16, KV_FP8_E4M3, KV_INT4 = 0, 1, 2
 
 
 class SinkAttnError(RuntimeError):
@@ -103,6 +104,7 @@ EXPORTS = (
     "sa_attn_decode_static", "sa_set_prefill_events", "sa_kv_cache_init_ring",
     "sa_kv_cache_init_fp8", "sa_rmsnorm_fold_weight", "sa_qkv_proj", "sa_out_proj",
     "sa_attn_backward", "sa_attn_backward_workspace_size", "sa_prefill_sched_slot",
+    "sa_kv_cache_init_int4", "sa_kv_read", "sa_attn_prefill_quant", "sa_attn_prefill_quant_workspace_size",
 )
 
 _lib = None
@@ -145,9 +147,14 @@ def lib():
         L.sa_attn_backward_workspace_size.restype = ctypes.c_size_t
         L.sa_attn_backward_workspace_size.argtypes = [i32, i32, i32]
         L.sa_prefill_sched_slot.argtypes = [ctypes.c_uint64, i32]
+        L.sa_kv_cache_init_int4.argtypes = [P(_KVCache), vp, vp, vp, vp, i32, i32, i32, i32, i32]
+        L.sa_kv_read.argtypes = [P(_KVCache), i64, i32, vp, P(i64), vp, P(i64), vp]
+        L.sa_attn_prefill_quant.argtypes = [P(_KVCache), P(_AttnArgs), vp, ctypes.c_size_t, vp]
+        L.sa_attn_prefill_quant_workspace_size.restype = ctypes.c_size_t
+        L.sa_attn_prefill_quant_workspace_size.argtypes = [P(_KVCache), i32, i32]
         for name in EXPORTS:
             if name not in ("sa_status_string", "sa_attn_decode_workspace_size",
-                            "sa_attn_backward_workspace_size"):
+                            "sa_attn_backward_workspace_size", "sa_attn_prefill_quant_workspace_size"):
                 getattr(L, name).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -224,25 +231,38 @@ class Snapshot:
 class KVCache:
     """One layer's KV cache, head-major [B, n_kv, cap, d] (torch-owned device
     memory): bf16 rows, or with ``fp8=True`` e4m3 codes (uint8) plus fp32
-    row scales ``k_scale``/``v_scale`` [B, n_kv, cap]. ``k_rows(start,
-    stop)`` views rows as [B, T, n_kv, d]; ``k_scales(start, stop)`` the
-    scales as [B, T, n_kv]."""
+    row scales ``k_scale``/``v_scale`` [B, n_kv, cap], or with ``int4=True``
+    4-bit codes [B, n_kv, cap, d/2] (uint8, the even element in the low half)
+    plus bf16 block scales [B, n_kv, cap, d/32]. ``read(start, stop)`` gives
+    rows of any format as bf16 [B, T, n_kv, d]; ``k_rows(start, stop)`` views
+    the stored rows as [B, T, n_kv, ...], ``k_scales(start, stop)`` the scales
+    as [B, T, n_kv, ...]. ``k``, ``v``, ``k_scale``, ``v_scale``: the caller's
+    own buffers (contiguous), allocated here when None."""
 
-    def __init__(self, B, cap, n_kv, d, device="cuda", k=None, v=None, ring=0, fp8=False):
-        shape = (B, n_kv, cap, d)
-        dt = torch.uint8 if fp8 else torch.bfloat16
+    def __init__(self, B, cap, n_kv, d, device="cuda", k=None, v=None, ring=0, fp8=False, int4=False,
+                 k_scale=None, v_scale=None):
+        if fp8 and int4:
+            raise ValueError("a cache is fp8 or int4, not both")
+        shape = (B, n_kv, cap, d // 2 if int4 else d)
+        dt = torch.uint8 if fp8 or int4 else torch.bfloat16
         self.k = k if k is not None else torch.zeros(shape, dtype=dt, device=device)
         self.v = v if v is not None else torch.zeros(shape, dtype=dt, device=device)
         assert tuple(self.k.shape) == shape and self.k.is_contiguous() and self.v.is_contiguous()
+        assert tuple(self.v.shape) == shape
         assert self.k.dtype == dt and self.v.dtype == dt
         self.raw = _KVCache()
         self.fp8 = bool(fp8)
-        if fp8:
-            self.k_scale = torch.zeros((B, n_kv, cap), dtype=torch.float32, device=self.k.device)
-            self.v_scale = torch.zeros((B, n_kv, cap), dtype=torch.float32, device=self.k.device)
-            _check(lib().sa_kv_cache_init_fp8(ctypes.byref(self.raw), _ptr(self.k), _ptr(self.v),
-                                              _ptr(self.k_scale), _ptr(self.v_scale), B, cap, n_kv, d,
-                                              int(ring)), "sa_kv_cache_init_fp8")
+        self.int4 = bool(int4)
+        if fp8 or int4:
+            sshape = (B, n_kv, cap) if fp8 else (B, n_kv, cap, d // 32)
+            sdt = torch.float32 if fp8 else torch.bfloat16
+            self.k_scale = k_scale if k_scale is not None else torch.zeros(sshape, dtype=sdt, device=self.k.device)
+            self.v_scale = v_scale if v_scale is not None else torch.zeros(sshape, dtype=sdt, device=self.k.device)
+            for t in (self.k_scale, self.v_scale):
+                assert tuple(t.shape) == sshape and t.dtype == sdt and t.is_contiguous()
+            name = "sa_kv_cache_init_fp8" if fp8 else "sa_kv_cache_init_int4"
+            _check(getattr(lib(), name)(ctypes.byref(self.raw), _ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
+                                        _ptr(self.v_scale), B, cap, n_kv, d, int(ring)), name)
         elif ring:
             _check(lib().sa_kv_cache_init_ring(ctypes.byref(self.raw), _ptr(self.k), _ptr(self.v), B, cap,
                                                n_kv, d, int(ring)), "sa_kv_cache_init_ring")
@@ -263,7 +283,7 @@ class KVCache:
         return self._rows(self.v, start, stop)
 
     def k_scales(self, start=0, stop=None):
-        """FP8 caches: K row scales of positions [start, stop) as [B, T, n_kv]."""
+        """FP8 and INT4 caches: K scales of positions [start, stop) as [B, T, n_kv(, d/32)]."""
         return self._rows(self.k_scale, start, stop)
 
     def v_scales(self, start=0, stop=None):
@@ -284,6 +304,26 @@ class KVCache:
         """kv_append: copy already-rotated k and v rows at [offset, offset + T)."""
         _check(lib().sa_kv_append(ctypes.byref(self.raw), _ptr(k_rot), _strides(k_rot), _ptr(v),
                                   _strides(v), k_rot.shape[1], _stream(self.k)), "sa_kv_append")
+
+    def read(self, start=0, stop=None, k_out=None, v_out=None):
+        """kv_read: positions [start, stop) as bf16 rows (k, v) [B, T, n_kv, d]
+        (stop None: the offset). k_out, v_out: bf16 views to write into."""
+        stop = self.raw.offset if stop is None else int(stop)
+        shape = (self.raw.B, stop - int(start), self.raw.n_kv, self.raw.d)
+        if shape[1] < 0:
+            raise ValueError("stop is below start")
+        outs = []
+        for name, t in (("k_out", k_out), ("v_out", v_out)):
+            if t is None:
+                t = torch.empty(shape, dtype=torch.bfloat16, device=self.k.device)
+            else:
+                _view4(name, t)
+                if tuple(t.shape) != shape:
+                    raise ValueError(f"{name} must be {shape}")
+            outs.append(t)
+        _check(lib().sa_kv_read(ctypes.byref(self.raw), int(start), shape[1], _ptr(outs[0]), _strides(outs[0]),
+                                _ptr(outs[1]), _strides(outs[1]), _raw_stream(self.k)), "sa_kv_read")
+        return tuple(outs)
 
     def snapshot(self):
         s = _Snapshot()
@@ -334,6 +374,30 @@ def attn_prefill(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=None, ro
         lse = torch.empty((B, n_q, T), dtype=torch.float32, device=q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
     _check(lib().sa_attn_prefill(ctypes.byref(cache.raw), ctypes.byref(a), _raw_stream(q)), "sa_attn_prefill")
+    return (out, lse) if return_lse else out
+
+
+def prefill_quant_workspace(cache, T, window=0):
+    """A workspace for attn_prefill_quant of T rows at the cache's offset."""
+    nb = int(lib().sa_attn_prefill_quant_workspace_size(ctypes.byref(cache.raw), int(T), int(window)))
+    return torch.empty(nb, dtype=torch.uint8, device=cache.k.device)
+
+
+def attn_prefill_quant(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=None, rope_fused=True,
+                       workspace=None, out=None, return_lse=False, lse=None):
+    """attn_prefill on an FP8 or INT4 cache: append the (rotated) k/v rows
+    quantised, attend q to rows [0, offset + T) as ``cache.read`` gives them."""
+    B, T, n_q, d = q.shape
+    if workspace is None:
+        workspace = prefill_quant_workspace(cache, T, window)
+    if out is None:
+        out = torch.empty((B, T, n_q, d), dtype=torch.bfloat16, device=q.device)
+    if return_lse and lse is None:
+        lse = torch.empty((B, n_q, T), dtype=torch.float32, device=q.device)
+    a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
+    _check(lib().sa_attn_prefill_quant(ctypes.byref(cache.raw), ctypes.byref(a), workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), _raw_stream(q)),
+           "sa_attn_prefill_quant")
     return (out, lse) if return_lse else out
 
 
