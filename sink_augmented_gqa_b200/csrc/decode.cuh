@@ -73,6 +73,8 @@ struct DecodeParams {
   float* cks;       // FP8 caches: row scales [B][n_kv][cap] of K and of V
   float* cvs;
   int S;
+  int box_rows;     // INT4 caches: rows of a TMA box (a whole stage; 128 on a ring),
+  int units;        // and stages of all (b, g) together, one at least for each
   int pf_stages;    // stages each CTA prefetches into L2 before waiting for its predecessor
   float scale_log2;
   int rope;
@@ -452,21 +454,23 @@ __device__ __forceinline__ void load_q_words(const __nv_bfloat16* qrow, int lane
   }
 }
 
-// The end of a decode CTA's work, shared by the decode kernels: merges the
-// consumer warps' partials in shared memory ([NCW][8 m | 8 l | 8*D O] fp32 at
-// C::OFF_RED) and, with S > 1, the splits' records. Called by the 32 * NCW
-// consumer threads, after a barrier behind the partials' stores.
+// The end of a decode CTA's work on one (b, g), shared by the decode kernels:
+// merges the consumer warps' partials in shared memory (red: [NCW][8 m | 8 l |
+// 8*D O] fp32) and, with S > 1 CTAs, the S records at recs (split: this CTA's)
+// through buf (shared memory that no copy uses; buf_bytes: at least a record).
+// merge_phase: phase of merge_bar's next use. Called by the 32 * NCW consumer
+// threads, after a barrier behind the partials' stores.
 template <int D, typename C>
-__device__ __forceinline__ void decode_finish(const DecodeParams& p, uint8_t* smem, uint32_t sbase,
-                                              uint32_t merge_bar, volatile int* flag, const float* sink_sm, int g,
-                                              int split, int b) {
+__device__ __forceinline__ void decode_finish(const DecodeParams& p, const float* red, const uint8_t* buf,
+                                              uint32_t buf_bytes, uint32_t merge_bar, uint32_t& merge_phase,
+                                              volatile int* flag, const float* sink_sm, int g, int b, int split,
+                                              int S, float* recs_g) {
   const int QM = p.q_mult;
-  const float* red = reinterpret_cast<const float*>(smem + C::OFF_RED);
   const float LN2 = 0.6931471805599453f;
   const int tid = threadIdx.x;  // 0 .. 32*NCW-1
   constexpr int NT = 32 * C::NCW;
   const int RF = p.rec_floats;
-  float* rec = p.ws_rec + (((long long)b * p.n_kv + g) * p.S + split) * RF;
+  float* rec = recs_g + (long long)split * RF;
   // two adjacent outputs (head n, dims d, d+1) per thread and pass
   for (int idx = 2 * tid; idx < QM * D; idx += 2 * NT) {
     const int n = idx / D, d = idx % D;
@@ -485,7 +489,7 @@ __device__ __forceinline__ void decode_finish(const DecodeParams& p, uint8_t* sm
       O1 += ov.y * f;
     }
     const int h = g * QM + n;
-    if (p.S == 1) {
+    if (S == 1) {
       const float sink2 = sink_sm[n];
       const float M2 = fmaxf(M, sink2);
       const float fo = ex2(M - M2);
@@ -501,7 +505,7 @@ __device__ __forceinline__ void decode_finish(const DecodeParams& p, uint8_t* sm
       }
     }
   }
-  if (p.S == 1) return;
+  if (S == 1) return;
 
   // The ticket: the barrier orders every thread's record stores before
   // thread 0's release; its acquire makes the other CTAs' records visible to
@@ -509,23 +513,23 @@ __device__ __forceinline__ void decode_finish(const DecodeParams& p, uint8_t* sm
   named_bar_sync(1, NT);
   if (tid == 0) {
     const int ticket = atom_add_acq_rel_gpu(p.ws_cnt + (b * p.n_kv + g), 1);
-    flag[1] = (ticket == p.S - 1) ? 1 : 0;
+    flag[1] = (ticket == S - 1) ? 1 : 0;
   }
   named_bar_sync(1, NT);
   if (!flag[1]) return;
 
-  // Merge the S records of (b, g). The K/V ring is idle now: one bulk copy
-  // per round brings as many records as it holds (normally all S) into it,
+  // Merge the S records of (b, g): one bulk copy per round brings as many
+  // records as buf holds (normally all S) into it,
   // so the tail pays one memory round trip instead of one per batch of
   // loads. A group of G adjacent lanes owns four outputs (head n, dims
   // d .. d+3); its lanes take every G-th record and combine by shuffles.
   // The running maximum starts at the sink (log2 units):
   // M = max(sink, m_s), l = e^{sink-M} + sum_s e^{m_s-M} l_s.
-  const int S = p.S;
   const uint32_t rec_bytes = (uint32_t)RF * 4u;
-  const int per_round = (int)(C::RING_BYTES / rec_bytes);
-  const float* recs = reinterpret_cast<const float*>(smem);
-  const char* gsrc = reinterpret_cast<const char*>(p.ws_rec + ((long long)b * p.n_kv + g) * S * RF);
+  const int per_round = (int)(buf_bytes / rec_bytes);
+  const float* recs = reinterpret_cast<const float*>(buf);
+  const uint32_t buf_addr = smem_u32(buf);
+  const char* gsrc = reinterpret_cast<const char*>(recs_g);
   const int nf4 = QM * D / 4;
   const int G = 2 * nf4 <= NT ? 2 : 1;   // lanes per output group
   const int f4 = tid / G, part = tid % G;
@@ -536,22 +540,22 @@ __device__ __forceinline__ void decode_finish(const DecodeParams& p, uint8_t* sm
   float M = sink_sm[n];
   float L = (M == -INFINITY) ? 0.f : 1.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0, r = 0; s0 < S; s0 += per_round, ++r) {
+  for (int s0 = 0; s0 < S; s0 += per_round, merge_phase ^= 1) {
     const int cnt = S - s0 < per_round ? S - s0 : per_round;
     if (tid == 0) {
       // the records were written by generic stores (other CTAs', acquired
-      // through the ticket) and the ring was last written the same way
+      // through the ticket) and buf was last written the same way
       fence_proxy_async_global();
       fence_proxy_async_smem();
       const uint32_t bytes = (uint32_t)cnt * rec_bytes;
       mbar_arrive_expect_tx(merge_bar, bytes);
       for (uint32_t o = 0; o < bytes; o += 32768u)
-        bulk_load(sbase + o, gsrc + (size_t)s0 * rec_bytes + o, bytes - o < 32768u ? bytes - o : 32768u,
+        bulk_load(buf_addr + o, gsrc + (size_t)s0 * rec_bytes + o, bytes - o < 32768u ? bytes - o : 32768u,
                   merge_bar);
     }
     // a wait that runs out is recorded in the status word; the copy is then
     // drained before the ring is read or this CTA exits
-    if (!mbar_wait(merge_bar, (uint32_t)(r & 1))) mbar_wait_drain(merge_bar, (uint32_t)(r & 1));
+    if (!mbar_wait(merge_bar, merge_phase)) mbar_wait_drain(merge_bar, merge_phase);
     float Mr = M;
     float4 ar = make_float4(0.f, 0.f, 0.f, 0.f);
     float Lr = 0.f;
@@ -596,7 +600,7 @@ __device__ __forceinline__ void decode_finish(const DecodeParams& p, uint8_t* sm
     acc.z = fmaf(acc.z, f, ar.z);
     acc.w = fmaf(acc.w, f, ar.w);
     M = Mr;
-    named_bar_sync(1, NT);   // the ring is read before the next round's copy overwrites it
+    named_bar_sync(1, NT);   // buf is read before the next round's copy overwrites it
   }
   if (owner && part == 0) {
     const int h = g * QM + n;
@@ -1044,7 +1048,10 @@ __global__ void __launch_bounds__(288, 2)
   }
   named_bar_sync(1, 32 * C::NCW);
 
-  decode_finish<D, C>(p, smem, sbase, merge_bar, flag, sink_sm, g, split, b);
+  uint32_t merge_phase = 0;
+  // the K/V ring is idle now and takes the records
+  decode_finish<D, C>(p, red, smem, C::RING_BYTES, merge_bar, merge_phase, flag, sink_sm, g, b, split, p.S,
+                      p.ws_rec + ((long long)b * p.n_kv + g) * p.S * p.rec_floats);
 }
 
 }  // namespace sa

@@ -128,22 +128,23 @@ bool make_codes_map(CUtensorMap* map, void* base, int d, int n_kv, long long row
   return r == CUDA_SUCCESS;
 }
 
-// INT4 caches: tensor map over the codes [B][n_kv][cap][d / 2] bytes exposing
-// rows [0, rows_valid), box {d / 2, 128, 1, 1}: 32- and 64-byte rows swizzled
-// over their width, 48-byte rows plain.
-bool make_i4_map(CUtensorMap* map, void* base, int d, int n_kv, long long rows_valid, int cap, int B) {
+// INT4 caches: tensor map over the codes [B][n_kv][cap][d / 2] bytes as lines
+// of 128 bytes (cap is a multiple of 16, so a head's rows are whole lines),
+// exposing those of rows [0, rows_valid), boxes of box_rows rows (a multiple of
+// 128, at most 256 lines). 128-byte swizzle, or plain for d = 96 (i4_off in csrc/decode_int4.cuh).
+bool make_i4_map(CUtensorMap* map, void* base, int d, int n_kv, long long rows_valid, int cap, int B,
+                 int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr || rows_valid < 1) return false;
   const int rowb = d / 2;
-  const cuuint64_t dims[4] = {(cuuint64_t)rowb, (cuuint64_t)rows_valid, (cuuint64_t)n_kv, (cuuint64_t)B};
-  const cuuint64_t strides[3] = {(cuuint64_t)rowb, (cuuint64_t)cap * rowb, (cuuint64_t)n_kv * cap * rowb};
-  const cuuint32_t box[4] = {(cuuint32_t)rowb, 128, 1, 1};
+  const cuuint64_t dims[4] = {128, (cuuint64_t)((rows_valid * rowb + 127) / 128), (cuuint64_t)n_kv, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {128, (cuuint64_t)cap * rowb, (cuuint64_t)n_kv * cap * rowb};
+  const cuuint32_t box[4] = {128, (cuuint32_t)(box_rows / 128 * rowb), 1, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  const CUtensorMapSwizzle sw = rowb == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
-                                : (rowb == 32 ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_NONE);
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, estr,
-                         CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                         CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         d == 96 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
@@ -555,18 +556,15 @@ int decode_rec_floats(int q_mult, int d) { return q_mult * d + (2 * q_mult + 3) 
 
 size_t decode_cnt_bytes(int B, int n_kv) { return (((size_t)B * n_kv * 8) + 255) / 256 * 256; }
 
-size_t decode_ws_bytes(int B, int n_kv, int q_mult, int d, int S) {
-  return decode_cnt_bytes(B, n_kv) + (size_t)B * n_kv * S * decode_rec_floats(q_mult, d) * 4;
+size_t decode_ws_bytes(int B, int n_kv, int q_mult, int d, long long records) {
+  return decode_cnt_bytes(B, n_kv) + (size_t)records * decode_rec_floats(q_mult, d) * 4;
 }
 
 // Cache rows per ring stage of decode_kernel<d, f8> or decode_i4_kernel<d>
 // (its Cfg::R).
 long long decode_stage_rows(int d, int kv_dtype) {
-  if (kv_dtype == SA_KV_INT4) {
-    static_assert(sa::DecodeI4Cfg<64>::R == 256 && sa::DecodeI4Cfg<96>::R == 256 && sa::DecodeI4Cfg<128>::R == 256,
-                  "one stage height for every head width");
-    return 256;
-  }
+  if (kv_dtype == SA_KV_INT4)
+    return d == 64 ? sa::DecodeI4Cfg<64>::R : (d == 96 ? sa::DecodeI4Cfg<96>::R : sa::DecodeI4Cfg<128>::R);
   const bool f8 = kv_dtype == SA_KV_FP8_E4M3;
   switch (d) {
     case 64: return f8 ? sa::DecodeCfgT<64, true>::R : sa::DecodeCfgT<64, false>::R;
@@ -577,20 +575,44 @@ long long decode_stage_rows(int d, int kv_dtype) {
 
 // The rows one decode call reads and how they are split over CTAs: the
 // launch and the allocation-free entry point's size check both take it from
-// here. lo_mask: first admitted key; lo: first row streamed (ring, FP8 and
-// INT4 stages start on multiples of the stage height, so no TMA box wraps a
-// ring and the scales start on their stage's first row).
+// here. lo_mask: first admitted key; lo: first row streamed (ring and FP8
+// stages start on multiples of the stage height, INT4 stages on multiples of
+// 128 rows, so no TMA box wraps a ring and the scales start on their stage's
+// first row).
 struct DecodePlan {
   long long lo_mask, lo;
-  int S;   // CTAs per (b, g)
+  int S;               // CTAs per (b, g); INT4: 0 for equal shares of all stages
+  long long units;     // INT4: stages of all (b, g), one at least for each
+  int ctas;            // INT4: CTAs of the launch
+  long long records;   // records in the workspace; 0: none is needed
 };
+
+// Stages that taking up another (b, g) costs a CTA of an INT4 decode.
+constexpr long long kI4Border = 4;
 
 DecodePlan plan_decode(const sa_kv_cache* c, const sa_attn_args* a) {
   const long long R = decode_stage_rows(c->d, c->kv_dtype);
   DecodePlan pl;
   pl.lo_mask = a->window > 0 ? (a->offset + 1 - a->window > 0 ? a->offset + 1 - a->window : 0) : 0;
-  pl.lo = (c->ring > 0 || c->kv_dtype != SA_KV_BF16) ? pl.lo_mask / R * R : pl.lo_mask;
-  pl.S = decode_splits(a->B, c->n_kv, a->offset - pl.lo, R);
+  const long long align = c->kv_dtype == SA_KV_INT4 ? 128 : R;
+  pl.lo = (c->ring > 0 || c->kv_dtype != SA_KV_BF16) ? pl.lo_mask / align * align : pl.lo_mask;
+  const long long bgs = (long long)a->B * c->n_kv, n = a->offset - pl.lo;
+  pl.S = decode_splits(a->B, c->n_kv, n, R);
+  pl.records = pl.S > 1 ? bgs * pl.S : 0;
+  pl.units = bgs * (n > 0 ? (n + R - 1) / R : 1);
+  pl.ctas = 0;
+  if (c->kv_dtype == SA_KV_INT4) {
+    // One wave, two CTAs per SM. S CTAs for each (b, g), or (when that leaves
+    // more to some than equal shares, a border counted in) equal shares.
+    const long long slots = 2LL * num_sms(), per = pl.units / bgs;
+    const long long S = per < slots / bgs ? per : slots / bgs;
+    const long long shares = pl.units < slots ? pl.units : slots;
+    const bool deal = S >= 1 && (per + S - 1) / S <= (pl.units + shares - 1) / shares + kI4Border;
+    pl.S = deal ? (int)S : 0;
+    pl.ctas = (int)(deal ? bgs * S : shares);
+    // CTA i's record of pair j is record i + j
+    pl.records = deal && S == 1 ? 0 : pl.ctas + bgs - 1;
+  }
   return pl;
 }
 
@@ -613,12 +635,12 @@ sa_status fill_decode(DecodeParams& p, const sa_kv_cache* c, const sa_attn_args*
   p.n_blocks = n_cache > 0 ? (n_cache + R - 1) / R : 0;
   // a lone CTA streams everything in order; with several, half of each
   // one's share is static and the rest dynamic
-  p.static_stages = p.S == 1 ? (int)p.n_blocks : (int)(p.n_blocks / (2 * p.S));
+  p.static_stages = p.S <= 1 ? (int)p.n_blocks : (int)(p.n_blocks / (2 * p.S));
   p.pf_stages = (int)((kDecodePrefetchBytes + stage_tx - 1) / stage_tx);
-  if (p.S > 1) {
-    if (ws == nullptr || !aligned16(ws) || ws_bytes < decode_ws_bytes(a->B, c->n_kv, q_mult, c->d, p.S))
-      return SA_ERR_WORKSPACE;
-  }
+  if (pl.units > INT32_MAX) return SA_ERR_SHAPE;
+  p.units = (int)pl.units;
+  if (pl.records > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < decode_ws_bytes(a->B, c->n_kv, q_mult, c->d, pl.records)))
+    return SA_ERR_WORKSPACE;
   p.q = static_cast<const __nv_bfloat16*>(a->q);
   p.qs0 = a->q_strides[0];
   p.qs2 = a->q_strides[2];
@@ -654,26 +676,26 @@ sa_status fill_decode(DecodeParams& p, const sa_kv_cache* c, const sa_attn_args*
   return SA_OK;
 }
 
-// Launches a decode kernel: grid n_kv x S x B, with programmatic stream
-// serialization: back-to-back decode launches (one per layer) overlap one
-// kernel's drain with the next one's launch and set-up; the kernel waits for
-// its predecessor before touching global memory.
+// Launches a decode kernel with programmatic stream serialization:
+// back-to-back decode launches (one per layer) overlap one kernel's drain with
+// the next one's launch and set-up; the kernel waits for its predecessor before
+// touching global memory.
 template <typename K, typename... A>
-sa_status launch_decode_kernel(K kernel, const sa_kv_cache* c, const DecodeParams& p, int threads, uint32_t smem,
-                               std::atomic<uint64_t>& smem_set, cudaStream_t stream, const A&... args) {
+sa_status launch_decode_kernel(K kernel, dim3 grid, int threads, uint32_t smem, std::atomic<uint64_t>& smem_set,
+                               cudaStream_t stream, const A&... args) {
   const sa_status sm = set_smem_once(kernel, smem, smem_set);
   if (sm != SA_OK) return sm;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3(c->n_kv, p.S, p.B);
+  lc.gridDim = grid;
   lc.blockDim = dim3(threads);
   lc.dynamicSmemBytes = smem;
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, args..., p);
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, args...);
   return (last_launch_status() == SA_OK && e == cudaSuccess) ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -706,8 +728,8 @@ sa_status launch_decode(const sa_kv_cache* c, const sa_attn_args* a, void* ws, s
     }
   }
   static std::atomic<uint64_t> smem_set{0};
-  return launch_decode_kernel(sa::decode_kernel<D, F8>, c, p, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, smem_set, stream, tmK,
-                              tmV, tmKS, tmVS);
+  return launch_decode_kernel(sa::decode_kernel<D, F8>, dim3(c->n_kv, p.S, a->B), Cfg::NUM_THREADS, Cfg::SMEM_BYTES,
+                              smem_set, stream, tmK, tmV, tmKS, tmVS, p);
 }
 
 template <int D>
@@ -717,18 +739,20 @@ sa_status launch_decode_i4(const sa_kv_cache* c, const sa_attn_args* a, void* ws
   DecodeParams p;
   const sa_status st = fill_decode(p, c, a, Cfg::R, Cfg::STAGE_TX, ws, ws_bytes);
   if (st != SA_OK) return st;
+  static_assert(Cfg::R % 128 == 0 && Cfg::R * Cfg::ROWB / 128 <= 256, "a stage is one box of whole lines");
+  p.box_rows = p.ring_cap > 0 ? 128 : Cfg::R;
   CUtensorMap tmK, tmV;
   memset(&tmK, 0, sizeof(tmK));
   memset(&tmV, 0, sizeof(tmV));
   if (p.n_blocks > 0) {
     const long long rows = p.ring_cap > 0 ? (long long)c->cap : p.off;
-    if (!make_i4_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B) ||
-        !make_i4_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B))
+    if (!make_i4_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, p.box_rows) ||
+        !make_i4_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B, p.box_rows))
       return SA_ERR_CUDA;
   }
   static std::atomic<uint64_t> smem_set{0};
-  return launch_decode_kernel(sa::decode_i4_kernel<D>, c, p, Cfg::NUM_THREADS, Cfg::SMEM_BYTES, smem_set, stream, tmK,
-                              tmV);
+  return launch_decode_kernel(sa::decode_i4_kernel<D>, dim3(plan_decode(c, a).ctas), Cfg::NUM_THREADS,
+                              Cfg::SMEM_BYTES, smem_set, stream, tmK, tmV, p);
 }
 
 // A run of T bf16 rows beside cache rows from position pos on (int4.cuh).
@@ -1294,8 +1318,9 @@ sa_status sa_attn_decode_static(sa_kv_cache* cache, const sa_attn_args* a, sa_st
   if (a->T != 1) return SA_ERR_INVALID_ARG;
   const int q_mult = a->n_q / cache->n_kv;
   if (q_mult > 8) return SA_ERR_SHAPE;
-  const int S = plan_decode(cache, a).S;   // the split the launch will use
-  if (S > 1 && decode_ws_bytes(a->B, cache->n_kv, q_mult, cache->d, S) > SA_DECODE_STATIC_SCRATCH_BYTES)
+  const long long records = plan_decode(cache, a).records;   // of the split the launch will use
+  if (records > 0 &&
+      decode_ws_bytes(a->B, cache->n_kv, q_mult, cache->d, records) > SA_DECODE_STATIC_SCRATCH_BYTES)
     return SA_ERR_WORKSPACE;
   void* scratch = nullptr;
   st = static_scratch(&scratch);
