@@ -73,8 +73,7 @@ struct DecodeParams {
   float* cks;       // FP8 caches: row scales [B][n_kv][cap] of K and of V
   float* cvs;
   int S;
-  int box_rows;     // INT4 caches: rows of a TMA box (a whole stage; 128 on a ring),
-  int units;        // and stages of all (b, g) together, one at least for each
+  int units;        // INT4 caches: 128-row units of all (b, g) together, one at least for each
   int pf_stages;    // stages each CTA prefetches into L2 before waiting for its predecessor
   float scale_log2;
   int rope;

@@ -1,16 +1,19 @@
-// One-token decode over an INT4 cache (int4.cuh): a producer warp and eight
-// consumer warps per CTA, two CTAs per SM, as decode_kernel (decode.cuh), but
-// with 4.5 bits an element the arithmetic per byte is about four times that
-// of a bf16 cache, so the codes go to the tensor cores with as few
-// instructions as possible, and all SMs get the same number of rows:
+// One-token decode over an INT4 cache (int4.cuh). As in decode_kernel
+// (decode.cuh) a producer warp streams the rows through a ring of stages and
+// the consumer warps attend them, but with 4.5 bits an element the arithmetic
+// per byte is about four times that of a bf16 cache: the kernel is bound by
+// the ALU pipe (half the issue rate), so the codes go to the tensor cores with
+// as few instructions as possible, and every SM gets the same number of rows.
 //
-// A (sequence, KV head) pair's rows are cut into stages. Where the CTAs can be
-// dealt out to the pairs evenly, each pair gets S of them; else the stages of
-// all pairs lie in one row and every CTA takes an equal, contiguous share
-// (plan_decode chooses). A share can end one pair, span several and begin
-// another: the producer streams on across the border while the consumers
-// merge what they have of a pair (decode_finish) and take up the next one's
-// queries.
+// One CTA per SM, 16 consumer warps that take 32 rows each of a 512-row stage
+// (with two CTAs of 8 per SM the scheduler's older one ran ahead and left the
+// other half of the SM's warps for the last fifth of the time). A (sequence,
+// KV head) pair's rows count in units of 128. Where the CTAs can be dealt out
+// to the pairs evenly, each pair gets S of them; else the units of all pairs
+// lie in one row and every CTA takes an equal, contiguous share (plan_decode
+// chooses). A share can end one pair, span several and begin another: the
+// producer streams on across the border while the consumers merge what they
+// have of a pair (decode_finish) and take up the next one's queries.
 //
 // S^T = K Q^T, m16n8k16 in f16, 16 keys on the M side, the group's heads on the
 // N side: a code word w (8 nibbles) gives four f16 pairs by masks and one
@@ -50,41 +53,53 @@ namespace sa {
 
 template <int D>
 struct DecodeI4Cfg {
-  static constexpr int NCW = 8;                 // consumer warps
-  // rows per consumer warp and stage, in tiles of 32
-  static constexpr int RW = (D == 64) ? 64 : 32;
-  static constexpr int R = RW * NCW;
+  static constexpr int NCW = 16;                // consumer warps, 32 rows of a stage each
+  static constexpr int UNIT = 128;              // rows that shares count in
+  static constexpr int R = 32 * NCW;            // rows per stage
   static constexpr int NB = D / kI4Block;       // blocks per row
   static constexpr int ROWB = D / 2;            // code bytes per row
   static constexpr uint32_t STAGE_BYTES = R * ROWB;
   static constexpr uint32_t SC_BYTES = R * NB * 2;   // K (or V) scales of one stage
-  static constexpr int NS = (D == 96) ? 3 : 2;
+  static constexpr int NS = (D == 64) ? 5 : (D == 96 ? 3 : 2);
   static constexpr uint32_t STAGE_TX = 2 * (STAGE_BYTES + SC_BYTES);
-  static constexpr int NUM_THREADS = 32 * (NCW + 1);
+  // five warpgroups: four of consumers and the producer's, which gives its
+  // registers to them (640 * 96 at launch, 512 * 104 + 128 * 40 after)
+  static constexpr int NUM_THREADS = 32 * (NCW + 4);
+  static constexpr int REGS_CONSUMER = 104, REGS_PRODUCER = 40;
+  // K codes of the stages, then a tile of 32 rows for the new row (row 0 valid);
+  // the same of V; scales likewise ([R][NB] bf16 a stage)
+  static constexpr uint32_t XTILE = (32 * ROWB + 1023) / 1024 * 1024;
   static constexpr uint32_t OFF_K = 0;
-  static constexpr uint32_t OFF_V = NS * STAGE_BYTES;
-  // the new row: a tile of codes and scales, row 0 valid
-  static constexpr uint32_t XTILE = 32 * ROWB;
-  static constexpr uint32_t OFF_XK = 2 * NS * STAGE_BYTES;
-  static constexpr uint32_t OFF_XV = OFF_XK + XTILE;
-  static constexpr uint32_t OFF_KS = OFF_XV + XTILE;             // [NS][R][NB] bf16
-  static constexpr uint32_t OFF_VS = OFF_KS + NS * SC_BYTES;
-  static constexpr uint32_t OFF_XS = OFF_VS + NS * SC_BYTES;     // [2][32][NB] bf16
+  static constexpr uint32_t OFF_XK = NS * STAGE_BYTES;
+  static constexpr uint32_t OFF_V = OFF_XK + XTILE;
+  static constexpr uint32_t OFF_XV = OFF_V + NS * STAGE_BYTES;
+  static constexpr uint32_t RING_BYTES = OFF_XK;                 // K's: takes the records of a merge
+  static constexpr uint32_t OFF_KS = OFF_XV + XTILE;
+  static constexpr uint32_t OFF_XS = OFF_KS + NS * SC_BYTES;
+  static constexpr uint32_t OFF_VS = OFF_XS + 32 * NB * 2;
+  static constexpr uint32_t OFF_XVS = OFF_VS + NS * SC_BYTES;
   // [NCW warps][8 m | 8 l | 8*D O] fp32, then the records of a merge
   static constexpr uint32_t RED_WARP = (16 + 8 * D) * 4;
-  static constexpr uint32_t OFF_RED = OFF_XS + 2 * 32 * NB * 2;
+  static constexpr uint32_t OFF_RED = OFF_XVS + 32 * NB * 2;
   static constexpr uint32_t RED_BYTES = NCW * RED_WARP;
-  static constexpr uint32_t OFF_Q = OFF_RED + RED_BYTES;   // 8 query rows and the new K row, rotated, bf16
-  static constexpr uint32_t OFF_BAR = OFF_Q + 9 * D * 2;
+  // the group's queries as fragment words [8][D / 8] uint4, the sums of their 8
+  // elements [8][D / 8] fp32, and their score scales [8]; the new K row, bf16
+  static constexpr uint32_t OFF_Q = OFF_RED + RED_BYTES;
+  static constexpr uint32_t OFF_QSUM = OFF_Q + 8 * D * 2;
+  static constexpr uint32_t OFF_HS = OFF_QSUM + D * 4;
+  static constexpr uint32_t OFF_XROW = OFF_HS + 32;
+  static constexpr uint32_t OFF_BAR = OFF_XROW + D * 2;
   static constexpr uint32_t OFF_MBAR = OFF_BAR + 8 * (2 * NS);
   static constexpr uint32_t OFF_FLAG = OFF_MBAR + 8;
   static constexpr uint32_t OFF_SINK = OFF_FLAG + 16;
   static constexpr uint32_t SMEM_BYTES = OFF_SINK + 32 + 1024;
-  static_assert(2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
-  static_assert(9 * (D / 16) <= 32 * NCW, "one thread per 16 elements of the rows to rotate");
-  static_assert(OFF_XK % 1024 == 0 && STAGE_BYTES % 1024 == 0 && (XTILE % 1024 == 0 || D == 96),
-                "swizzled tiles start on a multiple of their pattern");
-  static_assert(OFF_BAR % 16 == 0 && OFF_KS % 16 == 0 && OFF_RED % 16 == 0, "barriers and bulk copies");
+  static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per block");
+  static_assert(9 * 8 <= 96 && D / 16 <= 8, "three warps rotate the rows, eight lanes each");
+  static_assert(STAGE_BYTES % 1024 == 0, "swizzled tiles start on a multiple of their pattern");
+  static_assert(OFF_BAR % 16 == 0 && OFF_KS % 16 == 0 && OFF_VS % 16 == 0 && SC_BYTES % 16 == 0 && OFF_RED % 16 == 0,
+                "barriers and bulk copies");
+  static_assert(OFF_XV - OFF_XK == OFF_V - OFF_K && OFF_XVS - OFF_XS == OFF_VS - OFF_KS, "the new row's tile");
+  static_assert(RING_BYTES >= RED_WARP, "a record fits");
 };
 
 // Byte offset of 16-byte block blk of a row in a tile. The rows lie end to
@@ -118,28 +133,59 @@ __device__ __forceinline__ void mma_16816_bf16_0(float (&d)[4], uint32_t a0, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+// d = A B, bf16, 16 x 8 x 8.
+__device__ __forceinline__ void mma_1688_bf16_0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
+
+// Loads at addr + OFF bytes: the offset belongs to the instruction.
+template <uint32_t OFF>
+__device__ __forceinline__ void ldmatrix_x4_at(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr), "n"(OFF));
+}
+template <uint32_t OFF>
+__device__ __forceinline__ void ldmatrix_x4_trans_at(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr), "n"(OFF));
+}
+
 // A row's block scales as words (bf16 pairs; the last one's upper half 0 where
 // the blocks are odd), and block blk's of them as fp32.
-template <int NB>
+template <int NB, uint32_t OFF>
 __device__ __forceinline__ void i4_row_scales(uint32_t addr, uint32_t (&w)[(NB + 1) / 2]) {
   if constexpr (NB == 2) {
-    w[0] = ld_shared_u32(addr);
+    asm volatile("ld.shared.u32 %0, [%1 + %2];" : "=r"(w[0]) : "r"(addr), "n"(OFF));
   } else if constexpr (NB == 4) {
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2 + %3];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr), "n"(OFF));
   } else {
     uint16_t h[3];
-#pragma unroll
-    for (int i = 0; i < 3; ++i) asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h[i]) : "r"(addr + 2 * i));
+    asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(h[0]) : "r"(addr), "n"(OFF));
+    asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(h[1]) : "r"(addr), "n"(OFF + 2));
+    asm volatile("ld.shared.u16 %0, [%1 + %2];" : "=h"(h[2]) : "r"(addr), "n"(OFF + 4));
     w[0] = (uint32_t)h[0] | (uint32_t)h[1] << 16;
     w[1] = h[2];
   }
+}
+// The scales of rows 8 c + r, c < 4, from row r's address on.
+template <int NB, uint32_t OFF>
+__device__ __forceinline__ void i4_tile_scales(uint32_t addr, uint32_t (&w)[4][(NB + 1) / 2]) {
+  i4_row_scales<NB, OFF>(addr, w[0]);
+  i4_row_scales<NB, OFF + 16 * NB>(addr, w[1]);
+  i4_row_scales<NB, OFF + 32 * NB>(addr, w[2]);
+  i4_row_scales<NB, OFF + 48 * NB>(addr, w[3]);
 }
 __device__ __forceinline__ float i4_scale(const uint32_t* w, int blk) {
   return (blk & 1) ? bf16_hi(w[blk >> 1]) : bf16_lo(w[blk >> 1]);
 }
 
 // What a consumer warp keeps of its (b, g). Of heads 2 (lane % 4) + {0, 1}: the
-// score scale hs, what the sums are relative to (ref, see the head of this
+// score scale hs and 1 / hs, what the sums are relative to (ref, see the head of this
 // file; ref = m + er) and the unscaled score thr = (m + 8) / hs that moves it;
 // the running sum l and those of P' per block ps (both over this lane's keys).
 // qf: the query fragments, qo: the offset's. lim: 2^(E + 1) as a bf16 pair, er =
@@ -151,7 +197,7 @@ struct I4State {
   uint32_t qf[NB][4];
   uint32_t qo[2];
   uint32_t lim;
-  float er, hs[2], m[2], ref[2], thr[2], l[2];
+  float er, hs[2], rhs[2], m[2], ref[2], thr[2], l[2];
   float ps[NB][2], o[NB][2][4];
 };
 
@@ -165,36 +211,36 @@ __device__ __noinline__ uint32_t i4_raise(uint32_t mag) {
   return top | top << 16;
 }
 
-// One warp's 32 keys of a stage: codes at kst / vst plus this lane's offsets
-// off[blk] (of row `lane`), scales of the first row at ksc / vsc. With MASK,
-// keys below n_first and from n_valid on are masked (their scales may hold
-// anything).
-template <int D, bool MASK>
-__device__ __forceinline__ void decode_tile_i4(uint32_t kst, uint32_t vst, const uint32_t (&off)[D / 32],
-                                               uint32_t ksc, uint32_t vsc, int n_first, int n_valid, I4State<D>& z,
-                                               int lane) {
+// One warp's 32 keys of a stage: K codes at kst plus this lane's offsets
+// off[blk] (of row `lane`), V codes VC bytes behind; K scales of row lane / 4 at
+// ksc, V's VS bytes behind. With MASK, keys below n_first and from n_valid on
+// are masked (their scales may hold anything).
+template <int D, bool MASK, uint32_t VC, uint32_t VS>
+__device__ __forceinline__ void decode_tile_i4(uint32_t kst, const uint32_t (&off)[D / 32], uint32_t ksc, int n_first,
+                                               int n_valid, I4State<D>& z, int lane) {
   constexpr int NB = D / 32, NW = (NB + 1) / 2;
   constexpr uint32_t M0 = 0x000F000Fu, M1 = 0x00F000F0u;
   const int r = lane >> 2, t = lane & 3;
-  ksc += (uint32_t)(r * NB * 2);
-  vsc += (uint32_t)(r * NB * 2);
   bool ok[4];   // key 8 c + r
 #pragma unroll
   for (int c = 0; c < 4; ++c) ok[c] = !MASK || (8 * c + r >= n_first && 8 * c + r < n_valid);
   float s[2][4];   // keys 16 j + r (0, 1) and + 8 (2, 3), heads 2 t + {0, 1}
   uint32_t sw[4][NW];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) i4_row_scales<NB>(ksc + (uint32_t)(8 * c * NB * 2), sw[c]);
+  i4_tile_scales<NB, 0>(ksc, sw);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
+    if constexpr (NB == 2) {
+      mma_1688_bf16_0(s[j], sw[2 * j][0], sw[2 * j + 1][0], z.qo[0]);
+      continue;
+    }
     const uint32_t a0 = (NW == 2 && (t & 1)) ? sw[2 * j][NW - 1] : sw[2 * j][0];
     const uint32_t a1 = (NW == 2 && (t & 1)) ? sw[2 * j + 1][NW - 1] : sw[2 * j + 1][0];
-    mma_16816_bf16_0(s[j], a0, a1, NW == 1 ? 0u : a0, NW == 1 ? 0u : a1, z.qo[0], z.qo[1]);
+    mma_16816_bf16_0(s[j], a0, a1, a0, a1, z.qo[0], z.qo[1]);
   }
 #pragma unroll
   for (int blk = 0; blk < NB; ++blk) {
     uint32_t w[4];
-    ldmatrix_x4(kst + off[blk], w[0], w[1], w[2], w[3]);
+    ldmatrix_x4_at<0>(kst + off[blk], w);
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       float a[4];
@@ -211,9 +257,9 @@ __device__ __forceinline__ void decode_tile_i4(uint32_t kst, uint32_t vst, const
   }
   // the scales of V: E over them all
   uint32_t mag = 0;
+  i4_tile_scales<NB, VS>(ksc, sw);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    i4_row_scales<NB>(vsc + (uint32_t)(8 * c * NB * 2), sw[c]);
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
       if (MASK && !ok[c]) sw[c][i] = 0;   // a row never written holds anything
@@ -243,7 +289,7 @@ __device__ __forceinline__ void decode_tile_i4(uint32_t kst, uint32_t vst, const
       const float ref = z.m[e] == -INFINITY ? 0.f : z.m[e] + z.er;
       const float al = empty ? 0.f : ex2(z.ref[e] - ref);
       z.ref[e] = ref;
-      z.thr[e] = (z.m[e] + 8.f) / z.hs[e];
+      z.thr[e] = (z.m[e] + 8.f) * z.rhs[e];
       z.l[e] *= al;
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk) {
@@ -266,7 +312,7 @@ __device__ __forceinline__ void decode_tile_i4(uint32_t kst, uint32_t vst, const
 #pragma unroll
   for (int blk = 0; blk < NB; ++blk) {
     uint32_t x[4], pb[4];   // pb: P' of octet c, f16
-    ldmatrix_x4_trans(vst + off[blk], x[0], x[1], x[2], x[3]);
+    ldmatrix_x4_trans_at<VC>(kst + off[blk], x);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const float v = i4_scale(sw[c], blk);
@@ -293,55 +339,70 @@ __device__ __forceinline__ void i4_split3(float x, uint32_t (&part)[3]) {
   }
 }
 
-// Query fragments (B operand) from the group's rotated rows qs [QM][D]: head
-// lane / 4, elements 32 blk + 8 t + {0, 4}, {1, 5}, {2, 6}, {3, 7} (t = lane % 4);
-// and empty sums.
+// Eight lanes of a warp (ch = lane % 8; those with ch >= D / 16 idle) make one
+// query row's fragment words: x1, x2 its rotated elements 8 ch.. and D / 2 + 8
+// ch... qw, qsum: the row's entries of 8 elements each. Returns the row's score
+// scale.
 template <int D>
-__device__ __forceinline__ void i4_start(I4State<D>& z, const __nv_bfloat16* qs, int QM, float scale_log2, int lane) {
-  constexpr int NB = D / kI4Block;
-  const int n = lane >> 2, t = lane & 3;
-  float qv[NB][8];
+__device__ __forceinline__ float i4_query(uint4 x1, uint4 x2, int ch, uint4* qw, float* qsum, float scale_log2) {
+  float v[2][8];
+  const uint32_t w[2][4] = {{x1.x, x1.y, x1.z, x1.w}, {x2.x, x2.y, x2.z, x2.w}};
   float amax = 0.f;
 #pragma unroll
-  for (int blk = 0; blk < NB; ++blk) {
-    uint4 u = make_uint4(0, 0, 0, 0);
-    if (n < QM) u = *reinterpret_cast<const uint4*>(qs + n * D + 32 * blk + 8 * t);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      qv[blk][i] = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-      amax = fmaxf(amax, fabsf(qv[blk][i]));
+      v[h][i] = (i & 1) ? bf16_hi(w[h][i >> 1]) : bf16_lo(w[h][i >> 1]);
+      amax = fmaxf(amax, fabsf(v[h][i]));
     }
-  }
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  // the head's largest |q| goes to [2^14, 2^15)
+#pragma unroll
+  for (int i = 1; i < 8; i <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, i));
+  // the row's largest |q| goes to [2^14, 2^15)
   int eq = 0;
   if (amax > 0.f) {
     eq = (int)((__float_as_uint(amax) >> 23) & 0xFFu) - 127 - 14;
     eq = eq < -100 ? -100 : (eq > 100 ? 100 : eq);
   }
   const float down = __uint_as_float((uint32_t)(127 - eq) << 23);
-  const float hs = scale_log2 * __uint_as_float((uint32_t)(127 + eq) << 23) * 0x1p24f;
-  z.hs[0] = __shfl_sync(0xffffffffu, hs, 8 * t);
-  z.hs[1] = __shfl_sync(0xffffffffu, hs, 8 * t + 4);
-  uint32_t part[4][3] = {};   // of block blk's offset, bf16
 #pragma unroll
-  for (int blk = 0; blk < NB; ++blk) {
+  for (int h = 0; h < 2; ++h) {
     float sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      qv[blk][i] *= down;
-      sum += qv[blk][i];
+      v[h][i] *= down;
+      sum += v[h][i];
     }
+    if (ch < D / 16) {
+      // elements {0, 4}, {1, 5}, {2, 6}, {3, 7}; nibbles 1, 3, 5, 7 enter times 16
+      qw[ch + h * (D / 16)] = make_uint4(pack_f16(v[h][0], v[h][4]), pack_f16(v[h][1] * 0.0625f, v[h][5] * 0.0625f),
+                                         pack_f16(v[h][2], v[h][6]), pack_f16(v[h][3] * 0.0625f, v[h][7] * 0.0625f));
+      qsum[ch + h * (D / 16)] = sum;
+    }
+  }
+  return scale_log2 * __uint_as_float((uint32_t)(127 + eq) << 23) * 0x1p24f;
+}
+
+// A warp's share of the rows made by i4_query (B operand: head lane / 4, 8
+// elements t = lane % 4 of every block), and empty sums.
+template <int D>
+__device__ __forceinline__ void i4_start(I4State<D>& z, const uint4* qw, const float* qsum, const float* hs, int QM,
+                                         int lane) {
+  constexpr int NB = D / kI4Block;
+  const int n = lane >> 2, t = lane & 3;
+  uint32_t part[4][3] = {};   // of block blk's offset, bf16
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float f = (i & 1) ? 0.0625f : 1.f;   // nibbles 1, 3, 5, 7 enter times 16
-      z.qf[blk][i] = pack_f16(qv[blk][i] * f, qv[blk][i + 4] * f);
+  for (int blk = 0; blk < NB; ++blk) {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (n < QM) {
+      u = qw[n * (D / 8) + 4 * blk + t];
+      f = *reinterpret_cast<const float4*>(qsum + n * (D / 8) + 4 * blk);
     }
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    i4_split3(sum * (-8.0f * 0x1p-24f), part[blk]);
+    z.qf[blk][0] = u.x;
+    z.qf[blk][1] = u.y;
+    z.qf[blk][2] = u.z;
+    z.qf[blk][3] = u.w;
+    i4_split3(((f.x + f.y) + (f.z + f.w)) * (-8.0f * 0x1p-24f), part[blk]);
   }
   // The offset's B operand against a row's scale words w (A operand): two
   // blocks: lane t has w and part t; more: word t & 1, in register 0 part
@@ -361,6 +422,8 @@ __device__ __forceinline__ void i4_start(I4State<D>& z, const __nv_bfloat16* qs,
   z.lim = 0x13001300u;   // 2^-89, twice
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
+    z.hs[e] = 2 * t + e < QM ? hs[2 * t + e] : 1.f;
+    z.rhs[e] = __fdividef(1.f, z.hs[e]);
     z.m[e] = z.thr[e] = -INFINITY;
     z.ref[e] = 0.f;
     z.l[e] = 0.f;
@@ -402,12 +465,14 @@ __device__ __forceinline__ void i4_write_partial(const I4State<D>& z, float* rw,
   }
 }
 
-// tmK / tmV: the codes, dims {128, lines, n_kv, B} bytes. p.ck, p.cv, p.cks,
-// p.cvs hold the cache's code and scale arrays. p.units stages in all, per
-// pair p.units / (B n_kv); p.S > 0: S CTAs per pair, else equal shares.
+// tmK / tmV: the codes, dims {128, lines, n_kv, B} bytes, boxes of a stage's
+// rows; tmK1 / tmV1: the same with boxes of 128 rows. p.ck, p.cv, p.cks, p.cvs
+// hold the cache's code and scale arrays. p.units units of 128 rows in all, per
+// pair p.n_blocks (one at least); p.S > 0: S CTAs per pair, else equal shares.
 template <int D>
-__global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
+__global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
     decode_i4_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmK1, const __grid_constant__ CUtensorMap tmV1,
                      const DecodeParams p) {
   using C = DecodeI4Cfg<D>;
   constexpr int NB = C::NB, HALF = D / 2;
@@ -422,14 +487,17 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
   volatile int* flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
   // flag[0]: abort, flag[1]: "this CTA merges the pair's records"
   float* sink_sm = reinterpret_cast<float*>(smem + C::OFF_SINK);   // [q_mult] sinks, log2 units
-  __nv_bfloat16* q_sm = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_Q);
+  uint4* qw_sm = reinterpret_cast<uint4*>(smem + C::OFF_Q);
+  float* qsum_sm = reinterpret_cast<float*>(smem + C::OFF_QSUM);
+  float* hs_sm = reinterpret_cast<float*>(smem + C::OFF_HS);
+  __nv_bfloat16* x_sm = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_XROW);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int QM = p.q_mult;
-  const int per = p.n_blocks > 0 ? (int)p.n_blocks : 1;   // stages of a pair
+  const int per = p.n_blocks > 0 ? (int)p.n_blocks : 1;   // units of a pair
 
-  // This CTA's stages [u0, u1) of the row of all, and who holds stage u.
+  // This CTA's units [u0, u1) of the row of all, and who holds unit u.
   const int cta = blockIdx.x, base = p.units / (int)gridDim.x, rem = p.units - base * (int)gridDim.x;
   int u0, u1;
   if (p.S > 0) {
@@ -446,20 +514,34 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
   };
   int bg = u0 / per, b = bg / p.n_kv, g = bg - b * p.n_kv;
 
-  // Rows of scales to bring for a box of box_rows rows from position pos < off:
-  // whole 16-row groups up to the last cached one (cap is a multiple of 16).
-  const int box_rows = p.box_rows;
-  auto scale_rows = [&](long long pos) -> int {
-    if (p.ring_cap > 0) return box_rows;
-    const long long n = p.off - pos;
-    return n >= box_rows ? box_rows : (int)((n + 15) / 16 * 16);
+  // Brings rows [pos, pos + n) of pair (sequence b, KV head g), n > 0, through
+  // load(map, row, bytes of codes before, rows of the box) and scales(row,
+  // rows before, rows): one box for a whole stage of a linear cache, else
+  // boxes of 128 rows. pos is a multiple of 128 on a ring, whose capacity is
+  // one too, so that none wraps; scales come in whole groups of 16 rows (cap
+  // is a multiple of 16).
+  auto for_boxes = [&](long long pos, int n, auto&& load, auto&& scales) {
+    if (p.ring_cap == 0) {
+      if (n == C::R)
+        load(&tmK, &tmV, (int)pos, 0);
+      else
+        for (int r = 0; r < n; r += 128) load(&tmK1, &tmV1, (int)pos + r, r);
+      scales((int)pos, 0, (n + 15) / 16 * 16);
+    } else {
+      for (int r = 0; r < n; r += 128) {
+        const int row = (int)((pos + r) % p.ring_cap);
+        load(&tmK1, &tmV1, row, r);
+        scales(row, r, 128);
+      }
+    }
   };
   const char* ksc_g = reinterpret_cast<const char*>(p.cks);
   const char* vsc_g = reinterpret_cast<const char*>(p.cvs);
 
-  // The rows a pair's CTA rotates into q_sm, 16 elements (8 RoPE pairs) a
-  // thread: the group's queries, then the new K row. (sequence b, KV head g)
-  const int rot_row = threadIdx.x / (D / 16), rot_ch = threadIdx.x - rot_row * (D / 16);
+  // The rows that a CTA rotates for a pair, 16 elements (8 RoPE pairs) a
+  // thread, 8 lanes a row: the group's queries, then the new K row.
+  const int rot_row = threadIdx.x >> 3, rot_ch = threadIdx.x & 7;
+  const bool rot_in = rot_row <= QM && rot_ch < D / 16;
   auto rot_src = [&]() -> const __nv_bfloat16* {
     return 8 * rot_ch + (rot_row < QM ? p.q + b * p.qs0 + (long long)(g * QM + rot_row) * p.qs2
                                       : p.k + b * p.ks0 + (long long)g * p.ks2);
@@ -483,7 +565,7 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
   // The first rows go into L2 while the kernel before this one drains (a
   // prefetch brings nothing into the SM, so it is safe even if that kernel
   // writes some of them: L2 is where its writes land).
-  if (warp < C::NCW && rot_row <= QM) {
+  if (rot_in) {
     prefetch_l2(rot_src());
     if (D > 64) prefetch_l2(rot_src() + HALF);
     if (p.rope && rot_row == 0) {
@@ -494,20 +576,20 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
   if (warp == C::NCW && lane == 0 && p.n_blocks > 0) {
     tma_prefetch_desc(&tmK);
     tma_prefetch_desc(&tmV);
-    int k = u0 - bg * per;
-    for (int i = 0; i < p.pf_stages && i < u1 - u0 && k < per; ++i, ++k) {
-      const long long pos0 = p.lo + (long long)k * C::R;
-      for (int r = 0; r < C::R && pos0 + r < p.off; r += box_rows) {
-        const long long pos = pos0 + r;
-        const int row = (int)(p.ring_cap > 0 ? pos % p.ring_cap : pos);
-        const int line = row / 128 * C::ROWB;   // 128 rows are ROWB lines of 128 bytes
-        tma_prefetch_l2_4d(&tmK, 0, line, g, b);
-        tma_prefetch_l2_4d(&tmV, 0, line, g, b);
-        const uint32_t bytes = (uint32_t)scale_rows(pos) * NB * 2;
-        const long long so = ((long long)bg * p.cap + row) * NB * 2;
-        bulk_prefetch_l2(ksc_g + so, bytes);
-        bulk_prefetch_l2(vsc_g + so, bytes);
-      }
+    const int k0 = u0 - bg * per, k1 = min(per, u1 - bg * per);
+    for (int k = k0, i = 0; k < k1 && i < p.pf_stages; k += C::R / C::UNIT, ++i) {
+      const long long pos = p.lo + (long long)k * C::UNIT;
+      const int n = (int)min(min((long long)C::R, p.off - pos), (long long)(k1 - k) * C::UNIT);
+      for_boxes(pos, n,
+                [&](const CUtensorMap* mk, const CUtensorMap* mv, int row, int) {
+                  tma_prefetch_l2_4d(mk, 0, row / 128 * C::ROWB, g, b);   // 128 rows are ROWB lines
+                  tma_prefetch_l2_4d(mv, 0, row / 128 * C::ROWB, g, b);
+                },
+                [&](int row, int, int rows) {
+                  const long long so = ((long long)bg * p.cap + row) * NB * 2;
+                  bulk_prefetch_l2(ksc_g + so, (uint32_t)(rows * NB * 2));
+                  bulk_prefetch_l2(vsc_g + so, (uint32_t)(rows * NB * 2));
+                });
     }
   }
   __syncthreads();
@@ -515,37 +597,36 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
   // this one may still be using.
   griddep_wait();
 
-  if (warp == C::NCW) {
+  if (warp >= C::NCW) {
     // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      int k = u0 - bg * per;   // stage within the pair
-      const int n = u1 - u0;
+    regs_dec<C::REGS_PRODUCER>();
+    if (warp == C::NCW && lane == 0) {
       int it = 0;
-      for (; it < n && !flag[0]; ++it) {
+      for (int u = u0; u < u1 && !flag[0]; ++it) {
+        const int k = u - bg * per;   // unit within the pair
         const int s = it % C::NS;
-        if (!mbar_wait(empty_bar(s), (uint32_t)(((it / C::NS) & 1) ^ 1))) { flag[0] = 1; break; }
-        // one box a stage, or on a ring (whose capacity a stage need not divide)
-        // boxes of 128 rows that start on multiples of 128: none wraps
-        const long long pos0 = p.lo + (long long)k * C::R;
-        uint32_t tx = 0;
-        for (int r = 0; r < C::R && pos0 + r < p.off; r += box_rows)
-          tx += 2u * (uint32_t)(box_rows * C::ROWB + scale_rows(pos0 + r) * NB * 2);
-        mbar_arrive_expect_tx(full_bar(s), tx);
-        for (int r = 0; r < C::R && pos0 + r < p.off; r += box_rows) {
-          const long long pos = pos0 + r;
-          const int row = (int)(p.ring_cap > 0 ? pos % p.ring_cap : pos);
-          const uint32_t co = s * C::STAGE_BYTES + (uint32_t)(r * C::ROWB);
-          const int line = row / 128 * C::ROWB;
-          tma_load_4d(sbase + C::OFF_K + co, &tmK, full_bar(s), 0, line, g, b);
-          tma_load_4d(sbase + C::OFF_V + co, &tmV, full_bar(s), 0, line, g, b);
-          const uint32_t bytes = (uint32_t)scale_rows(pos) * NB * 2;
-          const long long so = ((long long)bg * p.cap + row) * NB * 2;
-          const uint32_t sd = s * C::SC_BYTES + (uint32_t)(r * NB * 2);
-          bulk_load(sbase + C::OFF_KS + sd, ksc_g + so, bytes, full_bar(s));
-          bulk_load(sbase + C::OFF_VS + sd, vsc_g + so, bytes, full_bar(s));
-        }
-        if (++k == per) {
-          k = 0;
+        if (!mbar_wait_asleep(empty_bar(s), (uint32_t)(((it / C::NS) & 1) ^ 1))) { flag[0] = 1; break; }
+        const int units = min(min(C::R / C::UNIT, per - k), u1 - u);
+        const long long pos = p.lo + (long long)k * C::UNIT;
+        const int n = (int)min((long long)units * C::UNIT, p.off - pos);   // 0: a pair without cached rows
+        const int boxes = (n + 127) / 128;
+        const int sc = p.ring_cap > 0 ? 128 * boxes : (n + 15) / 16 * 16;
+        mbar_arrive_expect_tx(full_bar(s), n > 0 ? 2u * (uint32_t)(128 * boxes * C::ROWB + sc * NB * 2) : 0u);
+        if (n > 0)
+          for_boxes(pos, n,
+                    [&](const CUtensorMap* mk, const CUtensorMap* mv, int row, int r) {
+                      const uint32_t co = s * C::STAGE_BYTES + (uint32_t)(r * C::ROWB);
+                      tma_load_4d(sbase + C::OFF_K + co, mk, full_bar(s), 0, row / 128 * C::ROWB, g, b);
+                      tma_load_4d(sbase + C::OFF_V + co, mv, full_bar(s), 0, row / 128 * C::ROWB, g, b);
+                    },
+                    [&](int row, int r, int rows) {
+                      const long long so = ((long long)bg * p.cap + row) * NB * 2;
+                      const uint32_t sd = s * C::SC_BYTES + (uint32_t)(r * NB * 2), bytes = (uint32_t)(rows * NB * 2);
+                      bulk_load(sbase + C::OFF_KS + sd, ksc_g + so, bytes, full_bar(s));
+                      bulk_load(sbase + C::OFF_VS + sd, vsc_g + so, bytes, full_bar(s));
+                    });
+        u += units;
+        if (k + units == per) {
           ++bg;
           if (++g == p.n_kv) {
             g = 0;
@@ -562,25 +643,35 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
   }
 
   // ---------------------------------------------------------------- consumers
-  uint32_t off[NB];   // this lane's ldmatrix row (row `lane` of the warp's first 32) in a stage
+  regs_inc<C::REGS_CONSUMER>();
+  uint32_t off[NB];   // this lane's ldmatrix row (row `lane` of the warp's) in a stage
 #pragma unroll
-  for (int blk = 0; blk < NB; ++blk) off[blk] = i4_off<D>(C::RW * warp + lane, blk);
-  uint32_t merge_phase = 0;
-  int it = 0;
+  for (int blk = 0; blk < NB; ++blk) off[blk] = i4_off<D>(32 * warp + lane, blk);
+  uint32_t merge_phase = 0, phase = 0;
+  int slot = 0;
   for (int u = u0; u < u1;) {
-    const int bg0 = bg * per;                       // the pair's first stage
+    const int bg0 = bg * per;                       // the pair's first unit
     const int end = min(u1, bg0 + per);
-    // the CTA with the pair's last stage attends the new row, in warp 0
+    // the CTA with the pair's last unit attends the new row, in warp 0
     const bool last_cta = end == bg0 + per, new_row = last_cta && warp == 0;
     {
       const float sink_in = (threadIdx.x < QM && p.sinks) ? p.sinks[g * QM + threadIdx.x] : -INFINITY;
-      if (rot_row < QM || (rot_row == QM && last_cta)) {
-        const __nv_bfloat16* src = rot_src();
-        uint4 x1 = *reinterpret_cast<const uint4*>(src), x2 = *reinterpret_cast<const uint4*>(src + HALF);
-        if (p.rope) rotate8(x1, x2, ctab, stab);
-        __nv_bfloat16* dst = q_sm + rot_row * D + 8 * rot_ch;
-        *reinterpret_cast<uint4*>(dst) = x1;
-        *reinterpret_cast<uint4*>(dst + HALF) = x2;
+      if (warp < 3) {
+        uint4 x1 = make_uint4(0, 0, 0, 0), x2 = x1;
+        if (rot_in && (rot_row < QM || last_cta)) {
+          const __nv_bfloat16* src = rot_src();
+          x1 = *reinterpret_cast<const uint4*>(src);
+          x2 = *reinterpret_cast<const uint4*>(src + HALF);
+          if (p.rope) rotate8(x1, x2, ctab, stab);
+          if (rot_row == QM) {
+            *reinterpret_cast<uint4*>(x_sm + 8 * rot_ch) = x1;
+            *reinterpret_cast<uint4*>(x_sm + HALF + 8 * rot_ch) = x2;
+          }
+        }
+        const int row = min(rot_row, 7);   // lanes past the queries write nothing
+        const float hs = i4_query<D>(x1, x2, rot_row < QM ? rot_ch : 8, qw_sm + row * (D / 8), qsum_sm + row * (D / 8),
+                                     p.scale_log2);
+        if (rot_row < QM && rot_ch == 0) hs_sm[rot_row] = hs;
       }
       if (threadIdx.x < QM) sink_sm[threadIdx.x] = sink_in * 1.4426950408889634f;
     }
@@ -592,11 +683,11 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
     if (n_live && n_is_v) na = *reinterpret_cast<const uint4*>(p.v + b * p.vs0 + (long long)g * p.vs2 + 8 * nch);
     named_bar_sync(1, 32 * C::NCW);
     I4State<D> z;
-    i4_start<D>(z, q_sm, QM, p.scale_log2, lane);
+    i4_start<D>(z, qw_sm, qsum_sm, hs_sm, QM, lane);
     // Quantise it, write it to the cache and stage it in smem as row 0 of a
     // tile (the other rows are masked).
     if (new_row) {
-      if (n_live && !n_is_v) na = *reinterpret_cast<const uint4*>(q_sm + QM * D + 8 * nch);
+      if (n_live && !n_is_v) na = *reinterpret_cast<const uint4*>(x_sm + 8 * nch);
       uint16_t sc;
       const uint32_t codes = i4_quantise8(na, sc);
       if (n_live) {
@@ -609,47 +700,47 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
                                      4 * (nch & 3)) = codes;
         if ((nch & 3) == 0) {
           *cs = sc;
-          reinterpret_cast<uint16_t*>(smem + C::OFF_XS)[(n_is_v ? 32 * NB : 0) + nch / 4] = sc;
+          reinterpret_cast<uint16_t*>(smem + (n_is_v ? C::OFF_XVS : C::OFF_XS))[nch / 4] = sc;
         }
       }
       __syncwarp();
     }
 
+    // The share's rows of this pair from position pos0 on: the first skip ones
+    // lie before the band. left and skip count from this warp's rows of a stage.
+    const int k0 = u - bg0, k_end = end - bg0;
+    const long long pos0 = p.lo + (long long)k0 * C::UNIT;
+    const int rows = (int)(min(p.off, p.lo + (long long)k_end * C::UNIT) - pos0);
+    int left = rows - 32 * warp, skip = (int)max(p.lo_mask - pos0, 0LL) - 32 * warp;
     // the stages, and for the warp with the new row its tile as one more
-    const int k_end = end - bg0;
-    for (int k = u - bg0; k < k_end + (new_row ? 1 : 0); ++k) {
-      if (flag[0]) break;
-      const bool is_new = k == k_end;
-      uint32_t kt = sbase + C::OFF_XK, vt = sbase + C::OFF_XV, ks = sbase + C::OFF_XS, vs = ks + 32 * NB * 2;
-      int first = 0, last = 1;
-      const int s = it % C::NS;
-      if (!is_new) {
-        if (!mbar_wait(full_bar(s), (uint32_t)((it / C::NS) & 1))) { flag[0] = 1; break; }
-        ++it;
-        // this warp's rows [first, last) of the stage are valid (the first ones
-        // may lie before the band, the last ones behind the cache)
-        const int r = C::RW * warp;
-        const long long pos = p.lo + (long long)k * C::R + r;
-        first = p.lo_mask > pos ? (int)(p.lo_mask - pos) : 0;
-        last = p.off - pos < C::RW ? (int)(p.off - pos) : C::RW;
-        kt = sbase + C::OFF_K + s * C::STAGE_BYTES;
-        vt = sbase + C::OFF_V + s * C::STAGE_BYTES;
-        ks = sbase + C::OFF_KS + s * C::SC_BYTES + (uint32_t)(r * NB * 2);
-        vs = sbase + C::OFF_VS + s * C::SC_BYTES + (uint32_t)(r * NB * 2);
+    const int n_st = (k_end - k0 + C::R / C::UNIT - 1) / (C::R / C::UNIT);
+    const int n_it = flag[0] ? 0 : n_st + (new_row ? 1 : 0);
+    for (int j = 0; j < n_it; ++j) {
+      // the new row's tile stands to V's as a stage does
+      uint32_t kt = sbase + C::OFF_XK, ks = sbase + C::OFF_XS;
+      if (j < n_st) {
+        if (!mbar_wait(full_bar(slot), phase)) { flag[0] = 1; break; }
+        kt = sbase + C::OFF_K + slot * C::STAGE_BYTES;
+        ks = sbase + C::OFF_KS + slot * C::SC_BYTES + (uint32_t)(32 * warp * NB * 2);
+      } else {
+        left = 1;
+        skip = 0;
       }
-      // 32 rows are a whole number of the swizzle's 1024-byte patterns (or of
-      // plain lines): a tile's offsets are the first one's plus its bytes
-      for (int i = 0; i < C::RW && i < last; i += 32) {
-        if (first <= i && i + 32 <= last)
-          decode_tile_i4<D, false>(kt + i * C::ROWB, vt + i * C::ROWB, off, ks + i * NB * 2, vs + i * NB * 2, 0, 32, z,
-                                   lane);
-        else if (first < i + 32 && first < last)
-          decode_tile_i4<D, true>(kt + i * C::ROWB, vt + i * C::ROWB, off, ks + i * NB * 2, vs + i * NB * 2, first - i,
-                                  last - i, z, lane);
-      }
-      if (!is_new) {
+      ks += (uint32_t)((lane >> 2) * NB * 2);
+      if (skip <= 0 && left >= 32)
+        decode_tile_i4<D, false, C::OFF_V - C::OFF_K, C::OFF_VS - C::OFF_KS>(kt, off, ks, 0, 32, z, lane);
+      else if (skip < min(left, 32))
+        decode_tile_i4<D, true, C::OFF_V - C::OFF_K, C::OFF_VS - C::OFF_KS>(kt, off, ks, max(skip, 0), min(left, 32),
+                                                                            z, lane);
+      if (j < n_st) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(empty_bar(s));
+        if (lane == 0) mbar_arrive(empty_bar(slot));
+        left -= C::R;
+        skip = 0;
+        if (++slot == C::NS) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
     }
     i4_write_partial<D>(z, reinterpret_cast<float*>(smem + C::OFF_RED) + warp * (C::RED_WARP / 4), lane);
@@ -661,7 +752,7 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 2)
     const int c_last = p.S > 0 ? c_first + p.S - 1 : holder(bg0 + per - 1);
     const bool idle = end == u1;   // the ring holds nothing to come: it takes the records
     decode_finish<D, C>(p, reinterpret_cast<const float*>(smem + C::OFF_RED), smem + (idle ? 0u : C::OFF_RED),
-                        idle ? C::OFF_XK : C::RED_BYTES, merge_bar, merge_phase, flag, sink_sm, g, b, cta - c_first,
+                        idle ? C::RING_BYTES : C::RED_BYTES, merge_bar, merge_phase, flag, sink_sm, g, b, cta - c_first,
                         c_last - c_first + 1, p.ws_rec + (long long)(c_first + bg) * p.rec_floats);
     u = end;
     if (u < u1) {

@@ -66,6 +66,30 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   }
 }
 
+// mbar_wait for a wait that is expected to last: the thread sleeps in the
+// barrier for up to a microsecond at a time (a hint) instead of asking again
+// at once, so it leaves the issue slots to the warps beside it.
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity) {
+  if (mbar_try(bar, parity)) return true;
+  const long long limit = *((volatile long long*)&g_wait_limit);
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(1000u)
+        : "memory");
+    if (ok) return true;
+    if (clock64() - t0 > limit) {
+      atomicOr(&g_status, STATUS_TIMEOUT);
+      return false;
+    }
+  }
+}
+
 // Bounded wait with a fixed limit (~1 s) that ignores the tunable one: used
 // only to drain work already in flight (TMA copies, queued MMAs) before a CTA
 // that aborted releases its shared or tensor memory. Such work always

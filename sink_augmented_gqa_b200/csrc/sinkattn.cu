@@ -560,12 +560,8 @@ size_t decode_ws_bytes(int B, int n_kv, int q_mult, int d, long long records) {
   return decode_cnt_bytes(B, n_kv) + (size_t)records * decode_rec_floats(q_mult, d) * 4;
 }
 
-// Cache rows per ring stage of decode_kernel<d, f8> or decode_i4_kernel<d>
-// (its Cfg::R).
-long long decode_stage_rows(int d, int kv_dtype) {
-  if (kv_dtype == SA_KV_INT4)
-    return d == 64 ? sa::DecodeI4Cfg<64>::R : (d == 96 ? sa::DecodeI4Cfg<96>::R : sa::DecodeI4Cfg<128>::R);
-  const bool f8 = kv_dtype == SA_KV_FP8_E4M3;
+// Cache rows per ring stage of decode_kernel<d, f8> (its Cfg::R).
+long long decode_stage_rows(int d, bool f8) {
   switch (d) {
     case 64: return f8 ? sa::DecodeCfgT<64, true>::R : sa::DecodeCfgT<64, false>::R;
     case 96: return f8 ? sa::DecodeCfgT<96, true>::R : sa::DecodeCfgT<96, false>::R;
@@ -576,43 +572,45 @@ long long decode_stage_rows(int d, int kv_dtype) {
 // The rows one decode call reads and how they are split over CTAs: the
 // launch and the allocation-free entry point's size check both take it from
 // here. lo_mask: first admitted key; lo: first row streamed (ring and FP8
-// stages start on multiples of the stage height, INT4 stages on multiples of
+// stages start on multiples of the stage height, INT4 units on multiples of
 // 128 rows, so no TMA box wraps a ring and the scales start on their stage's
 // first row).
 struct DecodePlan {
   long long lo_mask, lo;
   int S;               // CTAs per (b, g); INT4: 0 for equal shares of all stages
-  long long units;     // INT4: stages of all (b, g), one at least for each
+  long long units;     // INT4: 128-row units of all (b, g), one at least for each
   int ctas;            // INT4: CTAs of the launch
   long long records;   // records in the workspace; 0: none is needed
 };
 
-// Stages that taking up another (b, g) costs a CTA of an INT4 decode.
-constexpr long long kI4Border = 4;
+// Units of 128 rows that taking up another (b, g) costs a CTA of an INT4 decode
+// (merging and the next queries take ~5 us, in which an SM attends 2,000 rows).
+constexpr long long kI4Border = 16;
 
 DecodePlan plan_decode(const sa_kv_cache* c, const sa_attn_args* a) {
-  const long long R = decode_stage_rows(c->d, c->kv_dtype);
+  const bool i4 = c->kv_dtype == SA_KV_INT4;
+  const long long R = i4 ? 128 : decode_stage_rows(c->d, c->kv_dtype == SA_KV_FP8_E4M3);
   DecodePlan pl;
   pl.lo_mask = a->window > 0 ? (a->offset + 1 - a->window > 0 ? a->offset + 1 - a->window : 0) : 0;
-  const long long align = c->kv_dtype == SA_KV_INT4 ? 128 : R;
-  pl.lo = (c->ring > 0 || c->kv_dtype != SA_KV_BF16) ? pl.lo_mask / align * align : pl.lo_mask;
+  pl.lo = (c->ring > 0 || c->kv_dtype != SA_KV_BF16) ? pl.lo_mask / R * R : pl.lo_mask;
   const long long bgs = (long long)a->B * c->n_kv, n = a->offset - pl.lo;
-  pl.S = decode_splits(a->B, c->n_kv, n, R);
-  pl.records = pl.S > 1 ? bgs * pl.S : 0;
-  pl.units = bgs * (n > 0 ? (n + R - 1) / R : 1);
-  pl.ctas = 0;
-  if (c->kv_dtype == SA_KV_INT4) {
-    // One wave, two CTAs per SM. S CTAs for each (b, g), or (when that leaves
-    // more to some than equal shares, a border counted in) equal shares.
-    const long long slots = 2LL * num_sms(), per = pl.units / bgs;
-    const long long S = per < slots / bgs ? per : slots / bgs;
-    const long long shares = pl.units < slots ? pl.units : slots;
-    const bool deal = S >= 1 && (per + S - 1) / S <= (pl.units + shares - 1) / shares + kI4Border;
-    pl.S = deal ? (int)S : 0;
-    pl.ctas = (int)(deal ? bgs * S : shares);
-    // CTA i's record of pair j is record i + j
-    pl.records = deal && S == 1 ? 0 : pl.ctas + bgs - 1;
+  if (!i4) {
+    pl.S = decode_splits(a->B, c->n_kv, n, R);
+    pl.records = pl.S > 1 ? bgs * pl.S : 0;
+    pl.units = pl.ctas = 0;
+    return pl;
   }
+  // One wave, a CTA per SM. S CTAs for each (b, g), of a stage (4 units) at
+  // least, or (when that leaves more to some than equal shares, a border
+  // counted in) equal shares.
+  const long long per = n > 0 ? (n + R - 1) / R : 1, slots = num_sms();
+  pl.units = bgs * per;
+  const long long S = (per + 3) / 4 < slots / bgs ? (per + 3) / 4 : slots / bgs;
+  const long long shares = pl.units < slots ? pl.units : slots;
+  const bool deal = S >= 1 && (per + S - 1) / S <= (pl.units + shares - 1) / shares + kI4Border;
+  pl.S = deal ? (int)S : 0;
+  pl.ctas = (int)(deal ? bgs * S : shares);
+  pl.records = deal && S == 1 ? 0 : pl.ctas + bgs - 1;   // CTA i's record of pair j is record i + j
   return pl;
 }
 
@@ -737,22 +735,27 @@ sa_status launch_decode_i4(const sa_kv_cache* c, const sa_attn_args* a, void* ws
                            cudaStream_t stream) {
   using Cfg = sa::DecodeI4Cfg<D>;
   DecodeParams p;
-  const sa_status st = fill_decode(p, c, a, Cfg::R, Cfg::STAGE_TX, ws, ws_bytes);
+  const sa_status st = fill_decode(p, c, a, Cfg::UNIT, Cfg::STAGE_TX, ws, ws_bytes);
   if (st != SA_OK) return st;
-  static_assert(Cfg::R % 128 == 0 && Cfg::R * Cfg::ROWB / 128 <= 256, "a stage is one box of whole lines");
-  p.box_rows = p.ring_cap > 0 ? 128 : Cfg::R;
-  CUtensorMap tmK, tmV;
+  static_assert(Cfg::UNIT == 128 && Cfg::R % 128 == 0 && Cfg::R * Cfg::ROWB / 128 <= 256,
+                "a stage is one box of whole lines");
+  CUtensorMap tmK, tmV, tmK1, tmV1;
   memset(&tmK, 0, sizeof(tmK));
   memset(&tmV, 0, sizeof(tmV));
+  memset(&tmK1, 0, sizeof(tmK1));
+  memset(&tmV1, 0, sizeof(tmV1));
   if (p.n_blocks > 0) {
     const long long rows = p.ring_cap > 0 ? (long long)c->cap : p.off;
-    if (!make_i4_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, p.box_rows) ||
-        !make_i4_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B, p.box_rows))
+    // the large box is for linear caches with a stage of rows
+    if ((p.ring_cap == 0 && (!make_i4_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, Cfg::R) ||
+                             !make_i4_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B, Cfg::R))) ||
+        !make_i4_map(&tmK1, c->k, D, c->n_kv, rows, c->cap, c->B, 128) ||
+        !make_i4_map(&tmV1, c->v, D, c->n_kv, rows, c->cap, c->B, 128))
       return SA_ERR_CUDA;
   }
   static std::atomic<uint64_t> smem_set{0};
   return launch_decode_kernel(sa::decode_i4_kernel<D>, dim3(plan_decode(c, a).ctas), Cfg::NUM_THREADS,
-                              Cfg::SMEM_BYTES, smem_set, stream, tmK, tmV, p);
+                              Cfg::SMEM_BYTES, smem_set, stream, tmK, tmV, tmK1, tmV1, p);
 }
 
 // A run of T bf16 rows beside cache rows from position pos on (int4.cuh).
