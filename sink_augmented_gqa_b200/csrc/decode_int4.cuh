@@ -574,8 +574,8 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
     }
   }
   if (warp == C::NCW && lane == 0 && p.n_blocks > 0) {
-    tma_prefetch_desc(&tmK);
-    tma_prefetch_desc(&tmV);
+    tma_prefetch_desc(&tmK1);
+    tma_prefetch_desc(&tmV1);
     const int k0 = u0 - bg * per, k1 = min(per, u1 - bg * per);
     for (int k = k0, i = 0; k < k1 && i < p.pf_stages; k += C::R / C::UNIT, ++i) {
       const long long pos = p.lo + (long long)k * C::UNIT;

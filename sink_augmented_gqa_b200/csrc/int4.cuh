@@ -38,40 +38,39 @@ constexpr int kI4Block = 32;
 // Every lane of the warp takes part.
 __device__ __forceinline__ uint32_t i4_quantise8(uint4 v, uint16_t& scale) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  // 16-bit keys (magnitude << 1 | positive): their maximum is m, infinities
-  // and NaNs above every number
-  uint32_t key = 0;
+  // the block's largest and, negated, smallest element (NaN if one is)
+  const __nv_bfloat162* x2 = reinterpret_cast<const __nv_bfloat162*>(w);
+  __nv_bfloat162 hi = __hmax2_nan(__hmax2_nan(x2[0], x2[1]), __hmax2_nan(x2[2], x2[3]));
+  __nv_bfloat162 lo = __hmin2_nan(__hmin2_nan(x2[0], x2[1]), __hmin2_nan(x2[2], x2[3]));
+  const uint32_t hb = *reinterpret_cast<const uint32_t*>(&hi), lb = *reinterpret_cast<const uint32_t*>(&lo) ^ 0x80008000u;
+  const uint32_t pa = __byte_perm(hb, lb, 0x5410), pb = __byte_perm(hb, lb, 0x7632);
+  __nv_bfloat162 top = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&pa),
+                                   *reinterpret_cast<const __nv_bfloat162*>(&pb));   // {max, -min}
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    key = __vmaxu2(key, ((w[i] << 1) & 0xFFFEFFFEu) | ((~w[i] >> 15) & 0x00010001u));
-  key = __vmaxu2(key, __shfl_xor_sync(0xffffffffu, key, 1));
-  key = __vmaxu2(key, __shfl_xor_sync(0xffffffffu, key, 2));
-  key = max(key & 0xFFFFu, key >> 16);
-  const uint32_t mag = key >> 1;
-  if (mag >= 0x7F80u) {
-    scale = 0x7FC0u;
-    return 0x88888888u;
+  for (int i = 1; i < 4; i <<= 1) {
+    const uint32_t o = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&top), i);
+    top = __hmax2_nan(top, *reinterpret_cast<const __nv_bfloat162*>(&o));
   }
-  if (mag < 0x0380u) {   // 2^-120
-    scale = 0;
-    return 0x88888888u;
-  }
+  // |m| is the larger of the two and not negative; m < 0 where that is -min alone
+  const uint32_t tb = *reinterpret_cast<const uint32_t*>(&top);
+  const bool neg = bf16_hi(tb) > bf16_lo(tb);
+  const uint32_t mag = (neg ? tb >> 16 : tb) & 0x7FFFu;
   // |m| / 8 (three off the exponent, exact), then the 7 fraction bits rounded to 4
   uint32_t sb = mag - (3u << 7);
   sb = (sb + 3u + ((sb >> 3) & 1u)) & ~7u;
-  sb |= (key & 1u) << 15;
-  scale = (uint16_t)sb;
+  sb |= neg ? 0u : 0x8000u;
   // floor(x / s + 8.5) by the reciprocal: x and s have 8 and 5 significant
   // bits, so x / s + 8.5 is an integer or at least 2^-9 away from one (checked
-  // over all pairs), while fma(x, 1/s, .) is off by under 2^-18; with 2^-11
-  // added, rounding x / s + 8 to the nearest integer gives that floor.
-  const float r = __fdividef(1.0f, __uint_as_float(sb << 16));
+  // over all pairs), while the two products below are off by under 2^-18; with
+  // 2^-11 added, rounding x / s + 8 to the nearest integer gives that floor.
+  // The first product saturates to [0, 1], which is the clamp to [0, 15].
+  const float r = __fdividef(1.0f / 15.0f, __uint_as_float(sb << 16));
   constexpr float MAGIC = 12582912.0f;   // 1.5 * 2^23: its sum's low bits are the rounded integer
   uint32_t word = 0;
 #pragma unroll
   for (int i = 7; i >= 0; --i) {
     const float x = (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
-    const float y = fminf(fmaf(x, r, 8.0f + 0x1p-11f), 15.0f) + MAGIC;
+    const float y = fmaf(__saturatef(fmaf(x, r, (8.0f + 0x1p-11f) / 15.0f)), 15.0f, MAGIC);
     word = (word << 4) + __float_as_uint(y);
   }
   // each term carried MAGIC's own bits 0x4B400000, at shifts 0, 4, .., 28
@@ -80,7 +79,10 @@ __device__ __forceinline__ uint32_t i4_quantise8(uint4 v, uint16_t& scale) {
     for (int i = 0; i < 8; ++i) e = (e << 4) + 0x4B400000u;
     return e;
   }();
-  return word - EXTRA;
+  // no number to scale by: an infinity or NaN in the block, or |m| < 2^-120
+  const bool nan = mag >= 0x7F80u, zero = mag < 0x0380u;
+  scale = nan ? 0x7FC0u : (zero ? 0u : (uint16_t)sb);
+  return nan || zero ? 0x88888888u : word - EXTRA;
 }
 
 // 8 codes (a word, element i in bits 4i..) and their block's scale to bf16
@@ -113,44 +115,55 @@ struct RowsParams {
   long long ks0, ks1, ks2, vs0, vs1, vs2;
   int T, n_kv, cap;
   int row0;
-  int blocks_t;     // blocks of rows per (sequence, KV head)
 };
 
-// One thread per (row, 8 elements), K and V together; a block takes rows of
-// one (sequence, KV head), so its codes and scales are one contiguous run
-// and each row's 16-byte pieces are adjacent lanes.
+// A thread takes 8 elements of NR rows, K and V together, and has all of
+// their loads in flight before it works on the first; a block takes rows of one
+// (sequence, KV head), so its codes and scales are one contiguous run and each
+// row's 16-byte pieces are adjacent lanes. NR is 4 where that still gives
+// every SM a few blocks, else 1 (rows_per_thread).
 template <int D>
 struct RowsCfg {
   static constexpr int CH = D / 8;             // 8-element chunks of a row
-  static constexpr int RB = 256 / CH;          // rows per block
+  static constexpr int RB = 256 / CH;          // rows of a block at a time
   static constexpr int NB = D / kI4Block;
 };
 
 // Appends T bf16 rows to an INT4 cache.
-template <int D>
+template <int D, int NR>
 __global__ void __launch_bounds__(256) kv_append_i4_kernel(const RowsParams p) {
   using C = RowsCfg<D>;
-  const int bg = blockIdx.x / p.blocks_t;
-  const int ch = threadIdx.x % C::CH, rb = threadIdx.x / C::CH;
-  const int t = (blockIdx.x - bg * p.blocks_t) * C::RB + rb;
-  const int b = bg / p.n_kv, g = bg - b * p.n_kv;
-  const bool live = rb < C::RB && t < p.T;
-  uint4 kw = make_uint4(0, 0, 0, 0), vw = kw;
-  if (live) {
-    kw = *reinterpret_cast<const uint4*>(p.k + b * p.ks0 + t * p.ks1 + g * p.ks2 + 8 * ch);
-    vw = *reinterpret_cast<const uint4*>(p.v + b * p.vs0 + t * p.vs1 + g * p.vs2 + 8 * ch);
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int rb = threadIdx.x / C::CH, ch = threadIdx.x - rb * C::CH;
+  const int t0 = blockIdx.x * (C::RB * NR) + rb;
+  const long long row_bg = ((long long)b * p.n_kv + g) * p.cap;
+  const __nv_bfloat16* k = p.k + b * p.ks0 + g * p.ks2 + 8 * ch;
+  const __nv_bfloat16* v = p.v + b * p.vs0 + g * p.vs2 + 8 * ch;
+  uint4 kw[NR], vw[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int t = t0 + i * C::RB;
+    kw[i] = vw[i] = make_uint4(0, 0, 0, 0);
+    if (rb < C::RB && t < p.T) {
+      kw[i] = *reinterpret_cast<const uint4*>(k + t * p.ks1);
+      vw[i] = *reinterpret_cast<const uint4*>(v + t * p.vs1);
+    }
   }
-  uint16_t sk, sv;
-  const uint32_t ck = i4_quantise8(kw, sk), cv = i4_quantise8(vw, sv);
-  if (!live) return;
-  long long row = (long long)p.row0 + t;
-  if (row >= p.cap) row -= p.cap;
-  const long long at = (long long)bg * p.cap + row;
-  reinterpret_cast<uint32_t*>(const_cast<void*>(p.ck))[at * C::CH + ch] = ck;
-  reinterpret_cast<uint32_t*>(const_cast<void*>(p.cv))[at * C::CH + ch] = cv;
-  if ((ch & 3) == 0) {
-    reinterpret_cast<uint16_t*>(const_cast<void*>(p.cks))[at * C::NB + ch / 4] = sk;
-    reinterpret_cast<uint16_t*>(const_cast<void*>(p.cvs))[at * C::NB + ch / 4] = sv;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int t = t0 + i * C::RB;
+    uint16_t sk, sv;
+    const uint32_t ck = i4_quantise8(kw[i], sk), cv = i4_quantise8(vw[i], sv);
+    if (rb >= C::RB || t >= p.T) continue;
+    long long row = (long long)p.row0 + t;
+    if (row >= p.cap) row -= p.cap;
+    const long long at = row_bg + row;
+    reinterpret_cast<uint32_t*>(const_cast<void*>(p.ck))[at * C::CH + ch] = ck;
+    reinterpret_cast<uint32_t*>(const_cast<void*>(p.cv))[at * C::CH + ch] = cv;
+    if ((ch & 3) == 0) {
+      reinterpret_cast<uint16_t*>(const_cast<void*>(p.cks))[at * C::NB + ch / 4] = sk;
+      reinterpret_cast<uint16_t*>(const_cast<void*>(p.cvs))[at * C::NB + ch / 4] = sv;
+    }
   }
 }
 
@@ -165,27 +178,46 @@ __device__ __forceinline__ float f8_product(float code, float scale) {
   return __fmaf_rn(code, scale, -p) != 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
 }
 
-// Elements 8 ch.. of cache row `at` as bf16 pairs.
+// Elements 8 ch.. of cache row `at`: as stored, and as bf16 pairs.
+template <int KIND>
+struct StoredRow8 {
+  uint4 c;   // bf16 pairs, or codes (FP8: x, y; INT4: x)
+  float s;   // FP8: the row's scale
+  uint16_t h;  // INT4: the block's
+};
 template <int D, int KIND>
-__device__ __forceinline__ uint4 load_row8(const void* rows, const void* scales, long long at, int ch) {
+__device__ __forceinline__ StoredRow8<KIND> load_row8(const void* rows, const void* scales, long long at, int ch) {
   using C = RowsCfg<D>;
+  StoredRow8<KIND> x;
   if constexpr (KIND == ROWS_BF16) {
-    return *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(rows) + at * D + 8 * ch);
+    x.c = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(rows) + at * D + 8 * ch);
   } else if constexpr (KIND == ROWS_INT4) {
-    return i4_dequantise8(static_cast<const uint32_t*>(rows)[at * C::CH + ch],
-                          static_cast<const uint16_t*>(scales)[at * C::NB + ch / 4]);
+    x.c.x = static_cast<const uint32_t*>(rows)[at * C::CH + ch];
+    x.h = static_cast<const uint16_t*>(scales)[at * C::NB + ch / 4];
   } else {
     const uint2 c = static_cast<const uint2*>(rows)[at * C::CH + ch];
-    const float s = static_cast<const float*>(scales)[at];
+    x.c.x = c.x;
+    x.c.y = c.y;
+    x.s = static_cast<const float*>(scales)[at];
+  }
+  return x;
+}
+template <int KIND>
+__device__ __forceinline__ uint4 row8_bf16(const StoredRow8<KIND>& x) {
+  if constexpr (KIND == ROWS_BF16) {
+    return x.c;
+  } else if constexpr (KIND == ROWS_INT4) {
+    return i4_dequantise8(x.c.x, x.h);
+  } else {
     uint32_t r[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const uint32_t h = f16x2_from_e4m3x2((uint16_t)((i < 2 ? c.x : c.y) >> (16 * (i & 1))));
+      const uint32_t h = f16x2_from_e4m3x2((uint16_t)((i < 2 ? x.c.x : x.c.y) >> (16 * (i & 1))));
       const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      if (s >= 0x1p-90f) {
-        r[i] = pack_bf16(f8_product(f.x, s), f8_product(f.y, s));
+      if (x.s >= 0x1p-90f) {
+        r[i] = pack_bf16(f8_product(f.x, x.s), f8_product(f.y, x.s));
       } else {
-        r[i] = bf16_bits_from_f64((double)f.x * (double)s) | bf16_bits_from_f64((double)f.y * (double)s) << 16;
+        r[i] = bf16_bits_from_f64((double)f.x * (double)x.s) | bf16_bits_from_f64((double)f.y * (double)x.s) << 16;
       }
     }
     return make_uint4(r[0], r[1], r[2], r[3]);
@@ -193,20 +225,36 @@ __device__ __forceinline__ uint4 load_row8(const void* rows, const void* scales,
 }
 
 // Reads T positions of a cache back as bf16 rows.
-template <int D, int KIND>
+template <int D, int KIND, int NR>
 __global__ void __launch_bounds__(256) kv_read_kernel(const RowsParams p) {
   using C = RowsCfg<D>;
-  const int bg = blockIdx.x / p.blocks_t;
-  const int ch = threadIdx.x % C::CH, rb = threadIdx.x / C::CH;
-  const int t = (blockIdx.x - bg * p.blocks_t) * C::RB + rb;
-  if (rb >= C::RB || t >= p.T) return;
-  const int b = bg / p.n_kv, g = bg - b * p.n_kv;
-  long long row = (long long)p.row0 + t;
-  if (row >= p.cap) row -= p.cap;
-  const long long at = (long long)bg * p.cap + row;
-  const uint4 kw = load_row8<D, KIND>(p.ck, p.cks, at, ch), vw = load_row8<D, KIND>(p.cv, p.cvs, at, ch);
-  *reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.k) + b * p.ks0 + t * p.ks1 + g * p.ks2 + 8 * ch) = kw;
-  *reinterpret_cast<uint4*>(const_cast<__nv_bfloat16*>(p.v) + b * p.vs0 + t * p.vs1 + g * p.vs2 + 8 * ch) = vw;
+  const int g = blockIdx.y, b = blockIdx.z;
+  const int rb = threadIdx.x / C::CH, ch = threadIdx.x - rb * C::CH;
+  if (rb >= C::RB) return;
+  const int t0 = blockIdx.x * (C::RB * NR) + rb;
+  const long long row_bg = ((long long)b * p.n_kv + g) * p.cap;
+  StoredRow8<KIND> kr[NR], vr[NR];
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int t = t0 + i * C::RB;
+    long long row = (long long)p.row0 + t;
+    if (row >= p.cap) row -= p.cap;
+    const long long at = row_bg + row;
+    if (t < p.T) {
+      kr[i] = load_row8<D, KIND>(p.ck, p.cks, at, ch);
+      vr[i] = load_row8<D, KIND>(p.cv, p.cvs, at, ch);
+    }
+  }
+  __nv_bfloat16* k = const_cast<__nv_bfloat16*>(p.k) + b * p.ks0 + g * p.ks2 + 8 * ch;
+  __nv_bfloat16* v = const_cast<__nv_bfloat16*>(p.v) + b * p.vs0 + g * p.vs2 + 8 * ch;
+#pragma unroll
+  for (int i = 0; i < NR; ++i) {
+    const int t = t0 + i * C::RB;
+    if (t < p.T) {
+      *reinterpret_cast<uint4*>(k + t * p.ks1) = row8_bf16<KIND>(kr[i]);
+      *reinterpret_cast<uint4*>(v + t * p.vs1) = row8_bf16<KIND>(vr[i]);
+    }
+  }
 }
 
 }  // namespace sa

@@ -747,7 +747,7 @@ sa_status launch_decode_i4(const sa_kv_cache* c, const sa_attn_args* a, void* ws
   if (p.n_blocks > 0) {
     const long long rows = p.ring_cap > 0 ? (long long)c->cap : p.off;
     // the large box is for linear caches with a stage of rows
-    if ((p.ring_cap == 0 && (!make_i4_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, Cfg::R) ||
+    if ((p.ring_cap == 0 && p.off - p.lo >= Cfg::R && (!make_i4_map(&tmK, c->k, D, c->n_kv, rows, c->cap, c->B, Cfg::R) ||
                              !make_i4_map(&tmV, c->v, D, c->n_kv, rows, c->cap, c->B, Cfg::R))) ||
         !make_i4_map(&tmK1, c->k, D, c->n_kv, rows, c->cap, c->B, 128) ||
         !make_i4_map(&tmV1, c->v, D, c->n_kv, rows, c->cap, c->B, 128))
@@ -775,23 +775,46 @@ sa::RowsParams rows_params(const sa_kv_cache* c, const void* k, const int64_t ks
   p.n_kv = c->n_kv;
   p.cap = c->cap;
   p.row0 = (int)(c->ring > 0 ? pos % c->cap : pos);
-  p.blocks_t = (T + sa::RowsCfg<D>::RB - 1) / sa::RowsCfg<D>::RB;
   return p;
 }
 
-// Blocks of a row kernel; 0 when there are more than a grid holds.
-unsigned rows_grid(const sa_kv_cache* c, int blocks_t) {
-  const long long n = (long long)c->B * c->n_kv * blocks_t;
-  return n > INT32_MAX ? 0u : (unsigned)n;
+// Grid of a row kernel: blocks of rows x KV heads x sequences, with 4 rows a
+// thread where that still gives every SM four blocks (*four), else 1.
+template <int D>
+sa_status rows_grid(const sa_kv_cache* c, int T, dim3* grid, bool* four) {
+  constexpr int RB = sa::RowsCfg<D>::RB;
+  if (c->n_kv > 65535 || c->B > 65535) return SA_ERR_SHAPE;
+  const long long b4 = ((long long)T + 4 * RB - 1) / (4 * RB);
+  *four = (long long)c->B * c->n_kv * b4 >= 4LL * num_sms();
+  *grid = dim3((unsigned)(*four ? b4 : ((long long)T + RB - 1) / RB), c->n_kv, c->B);
+  return SA_OK;
 }
 
 template <int D>
 sa_status launch_append_i4(const sa_kv_cache* c, const void* k, const int64_t ks[3], const void* v,
                            const int64_t vs[3], int T, cudaStream_t stream) {
   const sa::RowsParams p = rows_params<D>(c, k, ks, v, vs, c->offset, T);
-  const unsigned grid = rows_grid(c, p.blocks_t);
-  if (grid == 0) return SA_ERR_SHAPE;
-  sa::kv_append_i4_kernel<D><<<grid, 256, 0, stream>>>(p);
+  dim3 grid;
+  bool four;
+  const sa_status st = rows_grid<D>(c, T, &grid, &four);
+  if (st != SA_OK) return st;
+  if (four)
+    sa::kv_append_i4_kernel<D, 4><<<grid, 256, 0, stream>>>(p);
+  else
+    sa::kv_append_i4_kernel<D, 1><<<grid, 256, 0, stream>>>(p);
+  return last_launch_status();
+}
+
+template <int D, int KIND>
+sa_status launch_read(const sa_kv_cache* c, const sa::RowsParams& p, cudaStream_t stream) {
+  dim3 grid;
+  bool four;
+  const sa_status st = rows_grid<D>(c, p.T, &grid, &four);
+  if (st != SA_OK) return st;
+  if (four)
+    sa::kv_read_kernel<D, KIND, 4><<<grid, 256, 0, stream>>>(p);
+  else
+    sa::kv_read_kernel<D, KIND, 1><<<grid, 256, 0, stream>>>(p);
   return last_launch_status();
 }
 
@@ -799,14 +822,11 @@ template <int D>
 sa_status launch_read(const sa_kv_cache* c, long long pos, void* k, const int64_t ks[3], void* v, const int64_t vs[3],
                       int T, cudaStream_t stream) {
   const sa::RowsParams p = rows_params<D>(c, k, ks, v, vs, pos, T);
-  const unsigned grid = rows_grid(c, p.blocks_t);
-  if (grid == 0) return SA_ERR_SHAPE;
   switch (c->kv_dtype) {
-    case SA_KV_INT4: sa::kv_read_kernel<D, sa::ROWS_INT4><<<grid, 256, 0, stream>>>(p); break;
-    case SA_KV_FP8_E4M3: sa::kv_read_kernel<D, sa::ROWS_FP8><<<grid, 256, 0, stream>>>(p); break;
-    default: sa::kv_read_kernel<D, sa::ROWS_BF16><<<grid, 256, 0, stream>>>(p); break;
+    case SA_KV_INT4: return launch_read<D, sa::ROWS_INT4>(c, p, stream);
+    case SA_KV_FP8_E4M3: return launch_read<D, sa::ROWS_FP8>(c, p, stream);
+    default: return launch_read<D, sa::ROWS_BF16>(c, p, stream);
   }
-  return last_launch_status();
 }
 
 sa_status launch_read(const sa_kv_cache* c, long long pos, void* k, const int64_t ks[3], void* v, const int64_t vs[3],

@@ -186,6 +186,16 @@ def _strides(t):
     return _I64x3(t.stride(0), t.stride(1), t.stride(2))
 
 
+def _empty4(B, T, H, d, device):
+    """A dense bf16 [B, T, H, d] tensor (empty_strided: the cheapest of
+    torch's allocating calls, and a decode step makes one per layer)."""
+    return torch.empty_strided((B, T, H, d), (T * H * d, H * d, d, 1), dtype=torch.bfloat16, device=device)
+
+
+def _empty_lse(B, n_q, T, device):
+    return torch.empty_strided((B, n_q, T), (n_q * T, T, 1), dtype=torch.float32, device=device)
+
+
 def _require_bf16_cuda(name, t):
     if t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA bf16 tensor")
@@ -302,28 +312,32 @@ class KVCache:
 
     def append(self, k_rot, v):
         """kv_append: copy already-rotated k and v rows at [offset, offset + T)."""
-        _check(lib().sa_kv_append(ctypes.byref(self.raw), _ptr(k_rot), _strides(k_rot), _ptr(v),
-                                  _strides(v), k_rot.shape[1], _stream(self.k)), "sa_kv_append")
+        ks, vs = _view4("k_rot", k_rot), _view4("v", v)
+        _check(lib().sa_kv_append(ctypes.byref(self.raw), k_rot.data_ptr(), _I64x3(ks[0], ks[1], ks[2]), v.data_ptr(),
+                                  _I64x3(vs[0], vs[1], vs[2]), k_rot.shape[1], _raw_stream(self.k)), "sa_kv_append")
 
     def read(self, start=0, stop=None, k_out=None, v_out=None):
         """kv_read: positions [start, stop) as bf16 rows (k, v) [B, T, n_kv, d]
         (stop None: the offset). k_out, v_out: bf16 views to write into."""
-        stop = self.raw.offset if stop is None else int(stop)
-        shape = (self.raw.B, stop - int(start), self.raw.n_kv, self.raw.d)
-        if shape[1] < 0:
+        raw = self.raw
+        start, stop = int(start), raw.offset if stop is None else int(stop)
+        B, T, H, d = raw.B, stop - start, raw.n_kv, raw.d
+        if T < 0:
             raise ValueError("stop is below start")
-        outs = []
-        for name, t in (("k_out", k_out), ("v_out", v_out)):
-            if t is None:
-                t = torch.empty(shape, dtype=torch.bfloat16, device=self.k.device)
-            else:
-                _view4(name, t)
-                if tuple(t.shape) != shape:
-                    raise ValueError(f"{name} must be {shape}")
-            outs.append(t)
-        _check(lib().sa_kv_read(ctypes.byref(self.raw), int(start), shape[1], _ptr(outs[0]), _strides(outs[0]),
-                                _ptr(outs[1]), _strides(outs[1]), _raw_stream(self.k)), "sa_kv_read")
-        return tuple(outs)
+        ks = vs = (T * H * d, H * d, d)
+        if k_out is None:
+            k_out = _empty4(B, T, H, d, self.k.device)
+        else:
+            ks = _view4("k_out", k_out)
+        if v_out is None:
+            v_out = _empty4(B, T, H, d, self.k.device)
+        else:
+            vs = _view4("v_out", v_out)
+        if k_out.shape != (B, T, H, d) or v_out.shape != (B, T, H, d):
+            raise ValueError(f"k_out and v_out must be {(B, T, H, d)}")
+        _check(lib().sa_kv_read(ctypes.byref(raw), start, T, k_out.data_ptr(), _I64x3(ks[0], ks[1], ks[2]),
+                                v_out.data_ptr(), _I64x3(vs[0], vs[1], vs[2]), _raw_stream(self.k)), "sa_kv_read")
+        return k_out, v_out
 
     def snapshot(self):
         s = _Snapshot()
@@ -369,9 +383,9 @@ def attn_prefill(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=None, ro
     [0, offset + T). Returns out [B,T,n_q,d] bf16 (and lse [B,n_q,T] fp32)."""
     B, T, n_q, d = q.shape
     if out is None:
-        out = torch.empty((B, T, n_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty4(B, T, n_q, d, q.device)
     if return_lse and lse is None:
-        lse = torch.empty((B, n_q, T), dtype=torch.float32, device=q.device)
+        lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
     _check(lib().sa_attn_prefill(ctypes.byref(cache.raw), ctypes.byref(a), _raw_stream(q)), "sa_attn_prefill")
     return (out, lse) if return_lse else out
@@ -391,9 +405,9 @@ def attn_prefill_quant(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=No
     if workspace is None:
         workspace = prefill_quant_workspace(cache, T, window)
     if out is None:
-        out = torch.empty((B, T, n_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty4(B, T, n_q, d, q.device)
     if return_lse and lse is None:
-        lse = torch.empty((B, n_q, T), dtype=torch.float32, device=q.device)
+        lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
     _check(lib().sa_attn_prefill_quant(ctypes.byref(cache.raw), ctypes.byref(a), workspace.data_ptr(),
                                        workspace.numel() * workspace.element_size(), _raw_stream(q)),
@@ -417,9 +431,9 @@ def attn_decode(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=None, rop
     if workspace is None:
         workspace = decode_workspace(B, n_q, cache.raw.n_kv, d, q.device)
     if out is None:
-        out = torch.empty((B, T, n_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty4(B, T, n_q, d, q.device)
     if return_lse and lse is None:
-        lse = torch.empty((B, n_q, T), dtype=torch.float32, device=q.device)
+        lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
     _check(lib().sa_attn_decode(ctypes.byref(cache.raw), ctypes.byref(a), workspace.data_ptr(),
                                 workspace.numel() * workspace.element_size(), _raw_stream(q)),
@@ -508,9 +522,9 @@ def attn_decode_static(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=No
     shared by every call -- do not overlap calls on the GPU."""
     B, T, n_q, d = q.shape
     if out is None:
-        out = torch.empty((B, T, n_q, d), dtype=torch.bfloat16, device=q.device)
+        out = _empty4(B, T, n_q, d, q.device)
     if return_lse and lse is None:
-        lse = torch.empty((B, n_q, T), dtype=torch.float32, device=q.device)
+        lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
     _check(lib().sa_attn_decode_static(ctypes.byref(cache.raw), ctypes.byref(a), _raw_stream(q)),
            "sa_attn_decode_static")
