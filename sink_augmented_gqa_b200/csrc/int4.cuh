@@ -178,6 +178,14 @@ __device__ __forceinline__ float f8_product(float code, float scale) {
   return __fmaf_rn(code, scale, -p) != 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
 }
 
+// A pair of e4m3 codes and their row's scale to a bf16 pair.
+__device__ __forceinline__ uint32_t f8_pair_bf16(uint16_t codes, float s) {
+  const uint32_t h = f16x2_from_e4m3x2(codes);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+  if (s >= 0x1p-90f) return pack_bf16(f8_product(f.x, s), f8_product(f.y, s));
+  return bf16_bits_from_f64((double)f.x * (double)s) | bf16_bits_from_f64((double)f.y * (double)s) << 16;
+}
+
 // Elements 8 ch.. of cache row `at`: as stored, and as bf16 pairs.
 template <int KIND>
 struct StoredRow8 {
@@ -211,15 +219,7 @@ __device__ __forceinline__ uint4 row8_bf16(const StoredRow8<KIND>& x) {
   } else {
     uint32_t r[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t h = f16x2_from_e4m3x2((uint16_t)((i < 2 ? x.c.x : x.c.y) >> (16 * (i & 1))));
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      if (x.s >= 0x1p-90f) {
-        r[i] = pack_bf16(f8_product(f.x, x.s), f8_product(f.y, x.s));
-      } else {
-        r[i] = bf16_bits_from_f64((double)f.x * (double)x.s) | bf16_bits_from_f64((double)f.y * (double)x.s) << 16;
-      }
-    }
+    for (int i = 0; i < 4; ++i) r[i] = f8_pair_bf16((uint16_t)((i < 2 ? x.c.x : x.c.y) >> (16 * (i & 1))), x.s);
     return make_uint4(r[0], r[1], r[2], r[3]);
   }
 }

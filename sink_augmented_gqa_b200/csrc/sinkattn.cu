@@ -21,6 +21,7 @@
 #include "int4.cuh"
 #include "prefill.cuh"
 #include "ptx.cuh"
+#include "quant_stage.cuh"
 #include "rope.cuh"
 
 namespace {
@@ -932,6 +933,66 @@ size_t quant_ws_bytes(const sa_kv_cache* c, int T, int window) {
   return 2 * (size_t)c->B * c->n_kv * (size_t)(quant_prefix(c, window) + T) * c->d * 2;
 }
 
+// The launch before the attention of sa_attn_prefill_quant: the call's rows into
+// cache c, the rows attended into the bf16 cache w (whose first row is position
+// lo of c), and with stage_q the rotated queries into a->out.
+template <int D, bool F8>
+sa_status launch_quant_stage(const sa_kv_cache* c, const sa_kv_cache* w, const sa_attn_args* a, long long lo,
+                             bool stage_q, cudaStream_t stream) {
+  using C = sa::RowsCfg<D>;
+  sa::QuantStageParams p;
+  p.ck = c->k;
+  p.cv = c->v;
+  p.cks = c->k_scale;
+  p.cvs = c->v_scale;
+  p.B = c->B;
+  p.n_kv = c->n_kv;
+  p.n_q = a->n_q;
+  p.cap = c->cap;
+  p.row_old = (int)(c->ring > 0 ? lo % c->cap : lo);
+  p.row_new = (int)(c->ring > 0 ? c->offset % c->cap : c->offset);
+  p.prefix = (int)(c->offset - lo);
+  p.T = a->T;
+  p.k = static_cast<const __nv_bfloat16*>(a->k);
+  p.v = static_cast<const __nv_bfloat16*>(a->v);
+  p.ks0 = a->k_strides[0]; p.ks1 = a->k_strides[1]; p.ks2 = a->k_strides[2];
+  p.vs0 = a->v_strides[0]; p.vs1 = a->v_strides[1]; p.vs2 = a->v_strides[2];
+  p.rope = a->rope_fused ? 1 : 0;
+  p.cos_t = a->rope_fused ? a->cos + c->offset * (D / 2) : nullptr;
+  p.sin_t = a->rope_fused ? a->sin + c->offset * (D / 2) : nullptr;
+  p.wk = static_cast<__nv_bfloat16*>(w->k);
+  p.wv = static_cast<__nv_bfloat16*>(w->v);
+  p.q = static_cast<const __nv_bfloat16*>(a->q);
+  p.qs0 = a->q_strides[0]; p.qs1 = a->q_strides[1]; p.qs2 = a->q_strides[2];
+  p.qo = static_cast<__nv_bfloat16*>(a->out);
+  p.os0 = a->out_strides[0]; p.os1 = a->out_strides[1]; p.os2 = a->out_strides[2];
+  p.blocks_new = (a->T + C::RB - 1) / C::RB;
+  p.blocks_old = (int)(((long long)p.prefix + 4 * C::RB - 1) / (4 * C::RB));
+  const long long bgs = (long long)c->B * c->n_kv, n_new = bgs * p.blocks_new, n_old = bgs * p.blocks_old;
+  const long long n_q = stage_q ? grid_for((long long)a->B * a->T * a->n_q * (D / 16)) : 0;
+  if (n_new + n_old + n_q > INT32_MAX) return SA_ERR_SHAPE;
+  p.n_new = (int)n_new;
+  p.n_old = (int)n_old;
+  sa::quant_stage_kernel<D, F8><<<(unsigned)(n_new + n_old + n_q), 256, 0, stream>>>(p);
+  return last_launch_status();
+}
+
+sa_status launch_quant_stage(const sa_kv_cache* c, const sa_kv_cache* w, const sa_attn_args* a, long long lo,
+                             bool stage_q, cudaStream_t stream) {
+  const bool f8 = c->kv_dtype == SA_KV_FP8_E4M3;
+  switch (c->d) {
+    case 64:
+      return f8 ? launch_quant_stage<64, true>(c, w, a, lo, stage_q, stream)
+                : launch_quant_stage<64, false>(c, w, a, lo, stage_q, stream);
+    case 96:
+      return f8 ? launch_quant_stage<96, true>(c, w, a, lo, stage_q, stream)
+                : launch_quant_stage<96, false>(c, w, a, lo, stage_q, stream);
+    default:
+      return f8 ? launch_quant_stage<128, true>(c, w, a, lo, stage_q, stream)
+                : launch_quant_stage<128, false>(c, w, a, lo, stage_q, stream);
+  }
+}
+
 // Scratch of sa_attn_decode_static: one fixed array per device, its device
 // address looked up once per device (host code may not use the symbol itself
 // as an address).
@@ -1289,17 +1350,9 @@ sa_status sa_attn_prefill_quant(sa_kv_cache* cache, const sa_attn_args* a, void*
   }
   bool appended = false;
   st = run_prefill(&w, &wa, s, [&](bool stage_q) -> sa_status {
-    // the call's rows, rotated, in the workspace; quantised from there into
-    // the cache; then all rows read back
-    sa_status r = launch_stage(&w, &wa, stage_q, s);
-    if (r != SA_OK) return r;
-    const int64_t ws[3] = {(int64_t)cache->n_kv * rows * cache->d, cache->d, rows * cache->d};
-    const long long row0 = prefix * cache->d;
-    __nv_bfloat16 *wk = static_cast<__nv_bfloat16*>(w.k), *wv = static_cast<__nv_bfloat16*>(w.v);
-    r = launch_append(cache, wk + row0, ws, wv + row0, ws, a->T, 0, nullptr, nullptr, s);
-    if (r != SA_OK) return r;
-    appended = true;
-    return launch_read(cache, lo, w.k, ws, w.v, ws, (int)rows, s);
+    const sa_status r = launch_quant_stage(cache, &w, a, lo, stage_q, s);
+    appended = r == SA_OK;
+    return r;
   });
   if (appended) note_append(cache, cache->offset, a->T);
   return st;
