@@ -125,7 +125,8 @@ __device__ __forceinline__ int band_window_start(const BandParams& p, int i0) {
 // halves trade their row maxima and sums through spare TMEM columns.
 // The queries of a pipeline's next unit are rotated while the tensor core
 // computes the current unit's O = P V.
-template <int D>
+// FINE: the polynomial exponentials to fp32 (exp2_fma2_fine).
+template <int D, bool FINE>
 __device__ __forceinline__ void band_softmax(const BandParams& p, uint8_t* smem, uint32_t bar0, uint32_t tmem,
                                              volatile int* abort_flag, int warp, int lane) {
   using C = BandCfg<D>;
@@ -268,7 +269,10 @@ __device__ __forceinline__ void band_softmax(const BandParams& p, uint8_t* smem,
         fma2(x2, x3, __uint_as_float(v[2 * c + 2]), __uint_as_float(v[2 * c + 3]), scale, scale, neg, neg);
         // one pair in four on the FMA pipe (polynomial exp2), the rest on MUFU
         if ((c / 2) % 2 == 0) {
-          exp2_fma2(x0, x1);
+          if constexpr (FINE)
+            exp2_fma2_fine(x0, x1);
+          else
+            exp2_fma2(x0, x1);
         } else {
           x0 = ex2(x0);
           x1 = ex2(x1);
@@ -332,7 +336,7 @@ __device__ __forceinline__ void band_softmax(const BandParams& p, uint8_t* smem,
   }
 }
 
-template <int D>
+template <int D, bool FINE>
 __global__ void __launch_bounds__(544, 1)
     band_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKw,
@@ -486,7 +490,7 @@ __global__ void __launch_bounds__(544, 1)
     }
     __syncwarp();
   } else {
-    band_softmax<D>(p, smem, bar0, tmem, abort_flag, warp, lane);
+    band_softmax<D, FINE>(p, smem, bar0, tmem, abort_flag, warp, lane);
   }
 
   tc_fence_before();

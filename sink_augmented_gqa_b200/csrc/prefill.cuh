@@ -254,7 +254,8 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint6
            (accumulate || kk > 0) ? 1u : 0u);
 }
 
-template <int D>
+// FINE: the polynomial exponentials to fp32 (exp2_fma2_fine).
+template <int D, bool FINE>
 __global__ void __launch_bounds__(384, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -645,7 +646,10 @@ __global__ void __launch_bounds__(384, 1)
             // One pair in four goes to the FMA pipe (polynomial exp2), the
             // rest to the MUFU unit: the two run side by side.
             if ((c / 2) % 2 == 0) {
-              exp2_fma2(x0, x1);
+              if constexpr (FINE)
+                exp2_fma2_fine(x0, x1);
+              else
+                exp2_fma2(x0, x1);
             } else {
               x0 = ex2(x0);
               x1 = ex2(x1);

@@ -397,7 +397,7 @@ sa_status with_sched_slot(cudaStream_t s, F&& launch) {
   return SA_OK;
 }
 
-template <int D>
+template <int D, bool FINE>
 sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, cudaStream_t stream) {
   using Cfg = PrefillCfg<D>;
   CUtensorMap tmQ, tmK, tmV;
@@ -443,7 +443,7 @@ sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, 
   p.ring_cap = c->ring > 0 ? c->cap : 0;
   static std::atomic<uint64_t> smem_set{0};
   {
-    const sa_status sm = set_smem_once(sa::prefill_kernel<D>, Cfg::SMEM_BYTES, smem_set);
+    const sa_status sm = set_smem_once(sa::prefill_kernel<D, FINE>, Cfg::SMEM_BYTES, smem_set);
     if (sm != SA_OK) return sm;
   }
   // persistent: one CTA per SM (or per item when there are fewer)
@@ -463,7 +463,7 @@ sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, 
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, sa::prefill_kernel<D>, tmQ, tmK, tmV, tmO, p);
+  const cudaError_t e = cudaLaunchKernelEx(&lc, sa::prefill_kernel<D, FINE>, tmQ, tmK, tmV, tmO, p);
   return (last_launch_status() == SA_OK && e == cudaSuccess) ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -480,6 +480,7 @@ int band_columns(const sa_kv_cache* c, const sa_attn_args* a) {
   return N <= sa::BandCfg<64>::NMAX ? N : 0;
 }
 
+template <bool FINE>
 sa_status launch_band(const sa_kv_cache* c, const sa_attn_args* a, int N, cudaStream_t stream) {
   using Cfg = sa::BandCfg<64>;
   const int qm = a->n_q / c->n_kv;
@@ -517,7 +518,7 @@ sa_status launch_band(const sa_kv_cache* c, const sa_attn_args* a, int N, cudaSt
   p.n_units = (int)units;
   static std::atomic<uint64_t> smem_set{0};
   {
-    const sa_status sm = set_smem_once(sa::band_kernel<64>, Cfg::SMEM_BYTES, smem_set);
+    const sa_status sm = set_smem_once(sa::band_kernel<64, FINE>, Cfg::SMEM_BYTES, smem_set);
     if (sm != SA_OK) return sm;
   }
   // persistent: one CTA per SM (or per unit when there are fewer)
@@ -532,7 +533,7 @@ sa_status launch_band(const sa_kv_cache* c, const sa_attn_args* a, int N, cudaSt
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, sa::band_kernel<64>, tmQ, tmK, tmV, tmKw, tmVw, tmO, p);
+  const cudaError_t e = cudaLaunchKernelEx(&lc, sa::band_kernel<64, FINE>, tmQ, tmK, tmV, tmKw, tmVw, tmO, p);
   return (last_launch_status() == SA_OK && e == cudaSuccess) ? SA_OK : SA_ERR_CUDA;
 }
 
@@ -891,8 +892,8 @@ sa_status launch_stage(sa_kv_cache* c, const sa_attn_args* a, bool stage_q, cuda
 
 // Prefill of the rows in a (T > 0) over bf16 cache c: stage(stage_q) puts the
 // call's K/V rows into c and, with stage_q, the rotated queries into a->out;
-// then the attention kernel.
-template <typename F>
+// then the attention kernel (FINE: its lse to fp32).
+template <bool FINE, typename F>
 sa_status run_prefill(const sa_kv_cache* c, const sa_attn_args* a, cudaStream_t s, F&& stage) {
   const cudaEvent_t ev0 = g_prefill_ev_before, ev1 = g_prefill_ev_after;
   const int band_n = band_columns(c, a);
@@ -902,7 +903,7 @@ sa_status run_prefill(const sa_kv_cache* c, const sa_attn_args* a, cudaStream_t 
     sa_status r = stage(false);
     if (r != SA_OK) return r;
     if (ev0 != nullptr && cudaEventRecord(ev0, s) != cudaSuccess) return SA_ERR_CUDA;
-    r = launch_band(c, a, band_n, s);
+    r = launch_band<FINE>(c, a, band_n, s);
     if (r == SA_OK && ev1 != nullptr && cudaEventRecord(ev1, s) != cudaSuccess) return SA_ERR_CUDA;
     return r;
   }
@@ -913,9 +914,9 @@ sa_status run_prefill(const sa_kv_cache* c, const sa_attn_args* a, cudaStream_t 
     if (r != SA_OK) return r;
     if (ev0 != nullptr && cudaEventRecord(ev0, s) != cudaSuccess) return SA_ERR_CUDA;
     switch (c->d) {
-      case 64: r = launch_prefill<64>(c, a, slot, s); break;
-      case 96: r = launch_prefill<96>(c, a, slot, s); break;
-      default: r = launch_prefill<128>(c, a, slot, s); break;
+      case 64: r = launch_prefill<64, FINE>(c, a, slot, s); break;
+      case 96: r = launch_prefill<96, FINE>(c, a, slot, s); break;
+      default: r = launch_prefill<128, FINE>(c, a, slot, s); break;
     }
     if (ev1 != nullptr && cudaEventRecord(ev1, s) != cudaSuccess) return SA_ERR_CUDA;
     return r;
@@ -1305,7 +1306,7 @@ sa_status sa_attn_prefill(sa_kv_cache* cache, const sa_attn_args* a, sa_stream_t
   bool staged = false;
   // one launch: the call's K rows rotated (when RoPE is fused) and appended
   // with V, and (stage_q) the rotated queries staged in `out`
-  st = run_prefill(cache, a, s, [&](bool stage_q) -> sa_status {
+  st = run_prefill<false>(cache, a, s, [&](bool stage_q) -> sa_status {
     const sa_status r = launch_stage(cache, a, stage_q, s);
     staged = r == SA_OK;
     return r;
@@ -1349,7 +1350,7 @@ sa_status sa_attn_prefill_quant(sa_kv_cache* cache, const sa_attn_args* a, void*
     wa.max_pos = (int32_t)(a->max_pos - lo);
   }
   bool appended = false;
-  st = run_prefill(&w, &wa, s, [&](bool stage_q) -> sa_status {
+  st = run_prefill<true>(&w, &wa, s, [&](bool stage_q) -> sa_status {
     const sa_status r = launch_quant_stage(cache, &w, a, lo, stage_q, s);
     appended = r == SA_OK;
     return r;

@@ -1,8 +1,12 @@
 """The INT4 row format: the oracle against brute force and closed forms (CPU)."""
 
+import os
+import re
+
 import numpy as np
 import pytest
 
+from sink_augmented_gqa_b200 import fit_exp2_poly as F
 from oracle import bf16 as obf16
 from oracle import int4 as oint4
 
@@ -84,10 +88,19 @@ def test_packing_and_bytes():
     assert oint4.kv_bytes_int4(24, 1, 131072, 8, 64) * 16 == 6 * 2 ** 30 * 4.5
 
 
+def test_fine_exp2_coefficients():
+    """The degree-4 polynomial of the prefill on quantised caches is what the
+    fit gives, within 3.5e-6 in fp32 Horner form."""
+    text = open(os.path.join(os.path.dirname(F.__file__), "csrc", "ptx.cuh")).read()
+    c = np.array([float(v) for _, v in sorted(re.findall(r"EXP2F_C(\d) = ([0-9.e+-]+)f", text))], dtype=np.float32)
+    np.testing.assert_allclose(c, F.fit(4), rtol=2e-6)
+    assert F.max_rel_error(c) < 3.5e-6
+
+
 def test_reciprocal_form_of_the_codes():
-    """The kernel's arithmetic, rounding fma(x, 1/s, 8 + 2^-11) to the nearest
-    integer, equals floor(x/s + 8.5) for every pair of significands, with a
-    reciprocal a few steps off."""
+    """The kernel's arithmetic, sat(fma(x, 1/(15 s), (8 + 2^-11) / 15)) times 15
+    rounded to the nearest integer, equals min(15, floor(x/s + 8.5)) for every
+    pair of significands, with a reciprocal a few steps off."""
     f = np.float32
     wrong = 0
     for M in range(128, 256):
@@ -99,9 +112,9 @@ def test_reciprocal_form_of_the_codes():
         xs = np.concatenate([xs, -xs, [0.0]])
         want = np.minimum(15, np.floor(xs / s + 8.5))
         for steps in (-2, 0, 2):
-            r = f(1) / f(s)
+            r = f(f(1 / 15) / f(s))
             for _ in range(abs(steps)):
                 r = np.nextafter(r, f(np.sign(steps) * 1e30))
-            y = np.minimum((xs * np.float64(r) + (8 + 2.0 ** -11)).astype(f), f(15))
-            wrong += int((np.rint(y) != want).sum())
+            y = np.clip((xs * np.float64(r) + np.float64(f((8 + 2.0 ** -11) / 15))).astype(f), 0, 1)
+            wrong += int((np.rint((np.float64(y) * 15).astype(f)) != want).sum())
     assert wrong == 0
