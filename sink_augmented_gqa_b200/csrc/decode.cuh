@@ -457,17 +457,16 @@ __device__ __forceinline__ void load_q_words(const __nv_bfloat16* qrow, int lane
 // merges the consumer warps' partials in shared memory (red: [NCW][8 m | 8 l |
 // 8*D O] fp32) and, with S > 1 CTAs, the S records at recs (split: this CTA's)
 // through buf (shared memory that no copy uses; buf_bytes: at least a record).
-// merge_phase: phase of merge_bar's next use. Called by the 32 * NCW consumer
-// threads, after a barrier behind the partials' stores.
-template <int D, typename C>
-__device__ __forceinline__ void decode_finish(const DecodeParams& p, const float* red, const uint8_t* buf,
+// merge_phase: phase of merge_bar's next use; merges: a word of shared memory.
+// Called by NT threads (tid), which meet at named barrier BAR, after a barrier
+// behind the partials' stores.
+template <int D, typename C, int NT, int BAR>
+__device__ __forceinline__ void decode_finish(const DecodeParams& p, int tid, const float* red, const uint8_t* buf,
                                               uint32_t buf_bytes, uint32_t merge_bar, uint32_t& merge_phase,
-                                              volatile int* flag, const float* sink_sm, int g, int b, int split,
+                                              volatile int* merges, const float* sink_sm, int g, int b, int split,
                                               int S, float* recs_g) {
   const int QM = p.q_mult;
   const float LN2 = 0.6931471805599453f;
-  const int tid = threadIdx.x;  // 0 .. 32*NCW-1
-  constexpr int NT = 32 * C::NCW;
   const int RF = p.rec_floats;
   float* rec = recs_g + (long long)split * RF;
   // two adjacent outputs (head n, dims d, d+1) per thread and pass
@@ -509,13 +508,13 @@ __device__ __forceinline__ void decode_finish(const DecodeParams& p, const float
   // The ticket: the barrier orders every thread's record stores before
   // thread 0's release; its acquire makes the other CTAs' records visible to
   // the merging CTA (whose thread 0 alone reads them, by bulk copy).
-  named_bar_sync(1, NT);
+  named_bar_sync(BAR, NT);
   if (tid == 0) {
     const int ticket = atom_add_acq_rel_gpu(p.ws_cnt + (b * p.n_kv + g), 1);
-    flag[1] = (ticket == S - 1) ? 1 : 0;
+    *merges = (ticket == S - 1) ? 1 : 0;
   }
-  named_bar_sync(1, NT);
-  if (!flag[1]) return;
+  named_bar_sync(BAR, NT);
+  if (!*merges) return;
 
   // Merge the S records of (b, g): one bulk copy per round brings as many
   // records as buf holds (normally all S) into it,
@@ -531,84 +530,91 @@ __device__ __forceinline__ void decode_finish(const DecodeParams& p, const float
   const char* gsrc = reinterpret_cast<const char*>(recs_g);
   const int nf4 = QM * D / 4;
   const int G = 2 * nf4 <= NT ? 2 : 1;   // lanes per output group
-  const int f4 = tid / G, part = tid % G;
-  const bool owner = f4 < nf4;
-  const int n = owner ? (4 * f4) / D : 0;
-  const int d = owner ? (4 * f4) % D : 0;
-  const int om = QM * D + n, ol = QM * D + QM + n, oo = n * D + d;
-  float M = sink_sm[n];
-  float L = (M == -INFINITY) ? 0.f : 1.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < S; s0 += per_round, merge_phase ^= 1) {
-    const int cnt = S - s0 < per_round ? S - s0 : per_round;
-    if (tid == 0) {
-      // the records were written by generic stores (other CTAs', acquired
-      // through the ticket) and buf was last written the same way
-      fence_proxy_async_global();
-      fence_proxy_async_smem();
-      const uint32_t bytes = (uint32_t)cnt * rec_bytes;
-      mbar_arrive_expect_tx(merge_bar, bytes);
-      for (uint32_t o = 0; o < bytes; o += 32768u)
-        bulk_load(buf_addr + o, gsrc + (size_t)s0 * rec_bytes + o, bytes - o < 32768u ? bytes - o : 32768u,
-                  merge_bar);
-    }
-    // a wait that runs out is recorded in the status word; the copy is then
-    // drained before the ring is read or this CTA exits
-    if (!mbar_wait(merge_bar, merge_phase)) mbar_wait_drain(merge_bar, merge_phase);
-    float Mr = M;
-    float4 ar = make_float4(0.f, 0.f, 0.f, 0.f);
-    float Lr = 0.f;
-    if (owner) {
-      float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-      int s2 = part;
-      for (; s2 + 3 * G < cnt; s2 += 4 * G) {
-        m0 = fmaxf(m0, recs[s2 * RF + om]);
-        m1 = fmaxf(m1, recs[(s2 + G) * RF + om]);
-        m2 = fmaxf(m2, recs[(s2 + 2 * G) * RF + om]);
-        m3 = fmaxf(m3, recs[(s2 + 3 * G) * RF + om]);
+  const int part = tid % G;
+  // (one pass of NT / G output groups, unless the threads are few)
+  for (int f0 = 0; f0 < nf4; f0 += NT / G) {
+    const int f4 = f0 + tid / G;
+    const bool owner = f4 < nf4;
+    const int n = owner ? (4 * f4) / D : 0;
+    const int d = owner ? (4 * f4) % D : 0;
+    const int om = QM * D + n, ol = QM * D + QM + n, oo = n * D + d;
+    float M = sink_sm[n];
+    float L = (M == -INFINITY) ? 0.f : 1.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < S; s0 += per_round) {
+      const int cnt = S - s0 < per_round ? S - s0 : per_round;
+      if (f0 == 0 || S > per_round) {   // else buf still holds them all
+        if (tid == 0) {
+          // the records were written by generic stores (other CTAs', acquired
+          // through the ticket) and buf was last written the same way
+          fence_proxy_async_global();
+          fence_proxy_async_smem();
+          const uint32_t bytes = (uint32_t)cnt * rec_bytes;
+          mbar_arrive_expect_tx(merge_bar, bytes);
+          for (uint32_t o = 0; o < bytes; o += 32768u)
+            bulk_load(buf_addr + o, gsrc + (size_t)s0 * rec_bytes + o, bytes - o < 32768u ? bytes - o : 32768u,
+                      merge_bar);
+        }
+        // a wait that runs out is recorded in the status word; the copy is then
+        // drained before the ring is read or this CTA exits
+        if (!mbar_wait(merge_bar, merge_phase)) mbar_wait_drain(merge_bar, merge_phase);
+        merge_phase ^= 1;
       }
-      for (; s2 < cnt; s2 += G) m0 = fmaxf(m0, recs[s2 * RF + om]);
-      Mr = fmaxf(fmaxf(Mr, fmaxf(m0, m1)), fmaxf(m2, m3));
-    }
-    if (G == 2) Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 1));
-    const float Mu = (Mr == -INFINITY) ? 0.f : Mr;
-    if (owner) {
+      float Mr = M;
+      float4 ar = make_float4(0.f, 0.f, 0.f, 0.f);
+      float Lr = 0.f;
+      if (owner) {
+        float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+        int s2 = part;
+        for (; s2 + 3 * G < cnt; s2 += 4 * G) {
+          m0 = fmaxf(m0, recs[s2 * RF + om]);
+          m1 = fmaxf(m1, recs[(s2 + G) * RF + om]);
+          m2 = fmaxf(m2, recs[(s2 + 2 * G) * RF + om]);
+          m3 = fmaxf(m3, recs[(s2 + 3 * G) * RF + om]);
+        }
+        for (; s2 < cnt; s2 += G) m0 = fmaxf(m0, recs[s2 * RF + om]);
+        Mr = fmaxf(fmaxf(Mr, fmaxf(m0, m1)), fmaxf(m2, m3));
+      }
+      if (G == 2) Mr = fmaxf(Mr, __shfl_xor_sync(0xffffffffu, Mr, 1));
+      const float Mu = (Mr == -INFINITY) ? 0.f : Mr;
+      if (owner) {
 #pragma unroll 4
-      for (int s2 = part; s2 < cnt; s2 += G) {
-        const float* rr = recs + s2 * RF;
-        const float w = ex2(rr[om] - Mu);
-        Lr = fmaf(w, rr[ol], Lr);
-        const float4 v = *reinterpret_cast<const float4*>(rr + oo);
-        ar.x = fmaf(w, v.x, ar.x);
-        ar.y = fmaf(w, v.y, ar.y);
-        ar.z = fmaf(w, v.z, ar.z);
-        ar.w = fmaf(w, v.w, ar.w);
+        for (int s2 = part; s2 < cnt; s2 += G) {
+          const float* rr = recs + s2 * RF;
+          const float w = ex2(rr[om] - Mu);
+          Lr = fmaf(w, rr[ol], Lr);
+          const float4 v = *reinterpret_cast<const float4*>(rr + oo);
+          ar.x = fmaf(w, v.x, ar.x);
+          ar.y = fmaf(w, v.y, ar.y);
+          ar.z = fmaf(w, v.z, ar.z);
+          ar.w = fmaf(w, v.w, ar.w);
+        }
       }
+      if (G == 2) {
+        Lr += __shfl_xor_sync(0xffffffffu, Lr, 1);
+        ar.x += __shfl_xor_sync(0xffffffffu, ar.x, 1);
+        ar.y += __shfl_xor_sync(0xffffffffu, ar.y, 1);
+        ar.z += __shfl_xor_sync(0xffffffffu, ar.z, 1);
+        ar.w += __shfl_xor_sync(0xffffffffu, ar.w, 1);
+      }
+      const float f = ex2(M - Mu);
+      L = fmaf(L, f, Lr);
+      acc.x = fmaf(acc.x, f, ar.x);
+      acc.y = fmaf(acc.y, f, ar.y);
+      acc.z = fmaf(acc.z, f, ar.z);
+      acc.w = fmaf(acc.w, f, ar.w);
+      M = Mr;
+      named_bar_sync(BAR, NT);   // buf is read before the next round's copy overwrites it
     }
-    if (G == 2) {
-      Lr += __shfl_xor_sync(0xffffffffu, Lr, 1);
-      ar.x += __shfl_xor_sync(0xffffffffu, ar.x, 1);
-      ar.y += __shfl_xor_sync(0xffffffffu, ar.y, 1);
-      ar.z += __shfl_xor_sync(0xffffffffu, ar.z, 1);
-      ar.w += __shfl_xor_sync(0xffffffffu, ar.w, 1);
+    if (owner && part == 0) {
+      const int h = g * QM + n;
+      const float inv = 1.0f / L;
+      uint2 packed;
+      packed.x = pack_bf16(acc.x * inv, acc.y * inv);
+      packed.y = pack_bf16(acc.z * inv, acc.w * inv);
+      *reinterpret_cast<uint2*>(p.out + b * p.os0 + (long long)h * p.os2 + d) = packed;
+      if (d == 0 && p.lse) p.lse[(long long)b * p.n_q + h] = (M + __log2f(L)) * LN2;
     }
-    const float f = ex2(M - Mu);
-    L = fmaf(L, f, Lr);
-    acc.x = fmaf(acc.x, f, ar.x);
-    acc.y = fmaf(acc.y, f, ar.y);
-    acc.z = fmaf(acc.z, f, ar.z);
-    acc.w = fmaf(acc.w, f, ar.w);
-    M = Mr;
-    named_bar_sync(1, NT);   // buf is read before the next round's copy overwrites it
-  }
-  if (owner && part == 0) {
-    const int h = g * QM + n;
-    const float inv = 1.0f / L;
-    uint2 packed;
-    packed.x = pack_bf16(acc.x * inv, acc.y * inv);
-    packed.y = pack_bf16(acc.z * inv, acc.w * inv);
-    *reinterpret_cast<uint2*>(p.out + b * p.os0 + (long long)h * p.os2 + d) = packed;
-    if (d == 0 && p.lse) p.lse[(long long)b * p.n_q + h] = (M + __log2f(L)) * LN2;
   }
   if (tid == 0) {
     p.ws_cnt[b * p.n_kv + g] = 0;
@@ -1049,8 +1055,9 @@ __global__ void __launch_bounds__(288, 2)
 
   uint32_t merge_phase = 0;
   // the K/V ring is idle now and takes the records
-  decode_finish<D, C>(p, red, smem, C::RING_BYTES, merge_bar, merge_phase, flag, sink_sm, g, b, split, p.S,
-                      p.ws_rec + ((long long)b * p.n_kv + g) * p.S * p.rec_floats);
+  decode_finish<D, C, 32 * C::NCW, 1>(p, threadIdx.x, red, smem, C::RING_BYTES, merge_bar, merge_phase, flag + 1,
+                                      sink_sm, g, b, split, p.S,
+                                      p.ws_rec + ((long long)b * p.n_kv + g) * p.S * p.rec_floats);
 }
 
 }  // namespace sa

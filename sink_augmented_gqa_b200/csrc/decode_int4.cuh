@@ -11,9 +11,12 @@
 // KV head) pair's rows count in units of 128. Where the CTAs can be dealt out
 // to the pairs evenly, each pair gets S of them; else the units of all pairs
 // lie in one row and every CTA takes an equal, contiguous share (plan_decode
-// chooses). A share can end one pair, span several and begin another: the
-// producer streams on across the border while the consumers merge what they
-// have of a pair (decode_finish) and take up the next one's queries.
+// chooses). A share can end one pair, span several and begin another. Nothing
+// of that holds up the rows: the producer streams on across the border, and
+// three warps beside it make the next pair's queries into fragments, quantise
+// the new row, and merge what the consumers left of the last pair
+// (decode_finish). The last pair of a CTA, with nothing behind it, the
+// consumers merge themselves.
 //
 // S^T = K Q^T, m16n8k16 in f16, 16 keys on the M side, the group's heads on the
 // N side: a code word w (8 nibbles) gives four f16 pairs by masks and one
@@ -62,44 +65,44 @@ struct DecodeI4Cfg {
   static constexpr uint32_t SC_BYTES = R * NB * 2;   // K (or V) scales of one stage
   static constexpr int NS = (D == 64) ? 5 : (D == 96 ? 3 : 2);
   static constexpr uint32_t STAGE_TX = 2 * (STAGE_BYTES + SC_BYTES);
-  // five warpgroups: four of consumers and the producer's, which gives its
-  // registers to them (640 * 96 at launch, 512 * 104 + 128 * 40 after)
+  // five warpgroups: four of consumers, one of the producer and the three
+  // warps beside it, which gives registers to the others (640 * 96 at launch,
+  // 512 * 104 + 128 * 64 after)
   static constexpr int NUM_THREADS = 32 * (NCW + 4);
-  static constexpr int REGS_CONSUMER = 104, REGS_PRODUCER = 40;
-  // K codes of the stages, then a tile of 32 rows for the new row (row 0 valid);
-  // the same of V; scales likewise ([R][NB] bf16 a stage)
+  static constexpr int HELPERS = 96;
+  static constexpr int REGS_CONSUMER = 104, REGS_PRODUCER = 64;
+  // K codes of the stages, then a tile of 32 rows for the new row (row 0
+  // valid); the same of V; scales likewise ([R][NB] bf16 a stage)
   static constexpr uint32_t XTILE = (32 * ROWB + 1023) / 1024 * 1024;
+  static constexpr uint32_t XSC = 32 * NB * 2;
   static constexpr uint32_t OFF_K = 0;
   static constexpr uint32_t OFF_XK = NS * STAGE_BYTES;
   static constexpr uint32_t OFF_V = OFF_XK + XTILE;
   static constexpr uint32_t OFF_XV = OFF_V + NS * STAGE_BYTES;
-  static constexpr uint32_t RING_BYTES = OFF_XK;                 // K's: takes the records of a merge
+  static constexpr uint32_t RING_BYTES = OFF_XK;                 // K's: takes the records of the last merge
   static constexpr uint32_t OFF_KS = OFF_XV + XTILE;
   static constexpr uint32_t OFF_XS = OFF_KS + NS * SC_BYTES;
-  static constexpr uint32_t OFF_VS = OFF_XS + 32 * NB * 2;
+  static constexpr uint32_t OFF_VS = OFF_XS + XSC;
   static constexpr uint32_t OFF_XVS = OFF_VS + NS * SC_BYTES;
   // [NCW warps][8 m | 8 l | 8*D O] fp32, then the records of a merge
   static constexpr uint32_t RED_WARP = (16 + 8 * D) * 4;
-  static constexpr uint32_t OFF_RED = OFF_XVS + 32 * NB * 2;
+  static constexpr uint32_t OFF_RED = OFF_XVS + XSC;
   static constexpr uint32_t RED_BYTES = NCW * RED_WARP;
-  // the group's queries as fragment words [8][D / 8] uint4, the sums of their 8
-  // elements [8][D / 8] fp32, and their score scales [8]; the new K row, bf16
+  // two pairs' queries: fragment words [8][D / 8] uint4, the sums of their 8
+  // elements [8][D / 8] fp32, score scales [8], sinks [8]
   static constexpr uint32_t OFF_Q = OFF_RED + RED_BYTES;
-  static constexpr uint32_t OFF_QSUM = OFF_Q + 8 * D * 2;
-  static constexpr uint32_t OFF_HS = OFF_QSUM + D * 4;
-  static constexpr uint32_t OFF_XROW = OFF_HS + 32;
+  static constexpr uint32_t Q_SUM = 8 * D * 2, Q_HS = Q_SUM + D * 4, Q_SINK = Q_HS + 32, Q_BYTES = Q_SINK + 32;
+  static constexpr uint32_t OFF_XROW = OFF_Q + 2 * Q_BYTES;      // the new K row, rotated, bf16
   static constexpr uint32_t OFF_BAR = OFF_XROW + D * 2;
-  static constexpr uint32_t OFF_MBAR = OFF_BAR + 8 * (2 * NS);
-  static constexpr uint32_t OFF_FLAG = OFF_MBAR + 8;
-  static constexpr uint32_t OFF_SINK = OFF_FLAG + 16;
-  static constexpr uint32_t SMEM_BYTES = OFF_SINK + 32 + 1024;
+  static constexpr uint32_t OFF_FLAG = OFF_BAR + 8 * (2 * NS + 7);
+  static constexpr uint32_t SMEM_BYTES = OFF_FLAG + 16 + 1024;
   static_assert(SMEM_BYTES <= 232448, "dynamic shared memory per block");
-  static_assert(9 * 8 <= 96 && D / 16 <= 8, "three warps rotate the rows, eight lanes each");
+  static_assert(9 * 8 <= HELPERS && D / 16 <= 8, "the helpers rotate the rows, eight lanes each");
   static_assert(STAGE_BYTES % 1024 == 0, "swizzled tiles start on a multiple of their pattern");
   static_assert(OFF_BAR % 16 == 0 && OFF_KS % 16 == 0 && OFF_VS % 16 == 0 && SC_BYTES % 16 == 0 && OFF_RED % 16 == 0,
                 "barriers and bulk copies");
   static_assert(OFF_XV - OFF_XK == OFF_V - OFF_K && OFF_XVS - OFF_XS == OFF_VS - OFF_KS, "the new row's tile");
-  static_assert(RING_BYTES >= RED_WARP, "a record fits");
+  static_assert(OFF_Q % 16 == 0 && Q_BYTES % 16 == 0 && OFF_BAR % 8 == 0, "alignment");
 };
 
 // Byte offset of 16-byte block blk of a row in a tile. The rows lie end to
@@ -483,14 +486,15 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
   const uint32_t bar0 = sbase + C::OFF_BAR;
   auto full_bar = [&](int s) -> uint32_t { return bar0 + 8u * (uint32_t)s; };
   auto empty_bar = [&](int s) -> uint32_t { return bar0 + 8u * (uint32_t)(C::NS + s); };
-  const uint32_t merge_bar = sbase + C::OFF_MBAR;
+  // a pair's queries ready (two buffers), its partials written, read again,
+  // its new row ready, and the barriers of the two merges' copies
+  auto q_bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)(2 * C::NS + (i & 1)); };
+  const uint32_t part_bar = bar0 + 8u * (2 * C::NS + 2), free_bar = part_bar + 8, row_bar = part_bar + 16,
+                 merge_bar = part_bar + 24, last_merge_bar = part_bar + 32;
+  // flag[0]: abort; flag[1], flag[2]: "this CTA merges the pair's records"
   volatile int* flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
-  // flag[0]: abort, flag[1]: "this CTA merges the pair's records"
-  float* sink_sm = reinterpret_cast<float*>(smem + C::OFF_SINK);   // [q_mult] sinks, log2 units
-  uint4* qw_sm = reinterpret_cast<uint4*>(smem + C::OFF_Q);
-  float* qsum_sm = reinterpret_cast<float*>(smem + C::OFF_QSUM);
-  float* hs_sm = reinterpret_cast<float*>(smem + C::OFF_HS);
-  __nv_bfloat16* x_sm = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_XROW);
+  const float* red = reinterpret_cast<const float*>(smem + C::OFF_RED);
+  auto q_buf = [&](int i) -> uint8_t* { return smem + C::OFF_Q + (uint32_t)(i & 1) * C::Q_BYTES; };
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -538,16 +542,28 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
   const char* ksc_g = reinterpret_cast<const char*>(p.cks);
   const char* vsc_g = reinterpret_cast<const char*>(p.cvs);
 
-  // The rows that a CTA rotates for a pair, 16 elements (8 RoPE pairs) a
+  // The rows that the helpers rotate for a pair, 16 elements (8 RoPE pairs) a
   // thread, 8 lanes a row: the group's queries, then the new K row.
-  const int rot_row = threadIdx.x >> 3, rot_ch = threadIdx.x & 7;
-  const bool rot_in = rot_row <= QM && rot_ch < D / 16;
+  const int htid = (int)threadIdx.x - 32 * (C::NCW + 1);
+  const int rot_row = htid >> 3, rot_ch = htid & 7;
+  const bool rot_in = htid >= 0 && rot_row <= QM && rot_ch < D / 16;
   auto rot_src = [&]() -> const __nv_bfloat16* {
     return 8 * rot_ch + (rot_row < QM ? p.q + b * p.qs0 + (long long)(g * QM + rot_row) * p.qs2
                                       : p.k + b * p.ks0 + (long long)g * p.ks2);
   };
   const float* ctab = p.cos_t + p.off * HALF + 8 * rot_ch;
   const float* stab = p.sin_t + p.off * HALF + 8 * rot_ch;
+  auto next_pair = [&]() {
+    ++bg;
+    if (++g == p.n_kv) {
+      g = 0;
+      ++b;
+    }
+  };
+  // The pair's CTAs. CTA c's record of pair bg is record c + bg of all: the
+  // shares' borders and the pairs' make one staircase.
+  auto first_cta = [&]() -> int { return p.S > 0 ? bg * p.S : holder(bg * per); };
+  auto last_cta = [&]() -> int { return p.S > 0 ? bg * p.S + p.S - 1 : holder(bg * per + per - 1); };
 
   // The next launch may take this CTA's slot as soon as it frees up; it does
   // its own set-up there and then waits for this grid to complete.
@@ -557,9 +573,16 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), C::NCW);
     }
+    mbar_init(q_bar(0), C::HELPERS / 32);
+    mbar_init(q_bar(1), C::HELPERS / 32);
+    mbar_init(part_bar, C::NCW);
+    mbar_init(free_bar, C::HELPERS / 32);
+    mbar_init(row_bar, 1);
     mbar_init(merge_bar, 1);
+    mbar_init(last_merge_bar, 1);
     flag[0] = 0;
     flag[1] = 0;
+    flag[2] = 0;
     fence_barrier_init();
   }
   // The first rows go into L2 while the kernel before this one drains (a
@@ -598,9 +621,10 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
   griddep_wait();
 
   if (warp >= C::NCW) {
-    // ------------------------------------------------------------ producer
     regs_dec<C::REGS_PRODUCER>();
-    if (warp == C::NCW && lane == 0) {
+    if (warp == C::NCW) {
+      // ------------------------------------------------------------ producer
+      if (lane != 0) return;
       int it = 0;
       for (int u = u0; u < u1 && !flag[0]; ++it) {
         const int k = u - bg * per;   // unit within the pair
@@ -626,20 +650,91 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
                       bulk_load(sbase + C::OFF_VS + sd, vsc_g + so, bytes, full_bar(s));
                     });
         u += units;
-        if (k + units == per) {
-          ++bg;
-          if (++g == p.n_kv) {
-            g = 0;
-            ++b;
-          }
-        }
+        if (k + units == per) next_pair();
       }
       if (flag[0]) {
         for (int j = (it > C::NS ? it - C::NS : 0); j < it; ++j)
           mbar_wait_drain(full_bar(j % C::NS), (uint32_t)((j / C::NS) & 1));
       }
+      return;
     }
-    return;  // the producer takes no part in the merges (named barriers below count 32*NCW)
+    // ------------------------------------------------------------ helpers
+    // prepare(i): the queries of this CTA's pair i, which is (b, g), into buffer
+    // i, and the new K row, rotated. The buffer's last readers, of pair i - 2,
+    // are through: their partials were waited for.
+    constexpr int CH = D / 8;   // 8 elements of the new row a lane of the first warp: lanes 0.. K, lanes 16.. V
+    const int nch = lane & 15;
+    const bool n_is_v = lane >= 16, n_live = htid < 32 && nch < CH;
+    __nv_bfloat16* x_sm = reinterpret_cast<__nv_bfloat16*>(smem + C::OFF_XROW);
+    auto prepare = [&](int i, bool last) {
+      uint8_t* qb = q_buf(i);
+      const float sink_in = (htid < QM && p.sinks) ? p.sinks[g * QM + htid] : -INFINITY;
+      uint4 x1 = make_uint4(0, 0, 0, 0), x2 = x1;
+      if (rot_in && (rot_row < QM || last)) {
+        const __nv_bfloat16* src = rot_src();
+        x1 = *reinterpret_cast<const uint4*>(src);
+        x2 = *reinterpret_cast<const uint4*>(src + HALF);
+        if (p.rope) rotate8(x1, x2, ctab, stab);
+        if (rot_row == QM) {
+          *reinterpret_cast<uint4*>(x_sm + 8 * rot_ch) = x1;
+          *reinterpret_cast<uint4*>(x_sm + HALF + 8 * rot_ch) = x2;
+        }
+      }
+      const int row = min(rot_row, 7);   // lanes past the queries write nothing
+      const float hs =
+          i4_query<D>(x1, x2, rot_row < QM ? rot_ch : 8, reinterpret_cast<uint4*>(qb) + row * (D / 8),
+                      reinterpret_cast<float*>(qb + C::Q_SUM) + row * (D / 8), p.scale_log2);
+      if (rot_row < QM && rot_ch == 0) reinterpret_cast<float*>(qb + C::Q_HS)[rot_row] = hs;
+      if (htid < QM) reinterpret_cast<float*>(qb + C::Q_SINK)[htid] = sink_in * 1.4426950408889634f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_bar(i));
+    };
+    // The new row of pair (b, g), quantised, into the cache and into smem as row
+    // 0 of a tile (whose other rows are masked). Its last reader, of the pair
+    // before, is through.
+    auto put_row = [&]() {
+      uint4 na = make_uint4(0, 0, 0, 0);
+      if (n_live && n_is_v) na = *reinterpret_cast<const uint4*>(p.v + b * p.vs0 + (long long)g * p.vs2 + 8 * nch);
+      named_bar_sync(2, C::HELPERS);   // x_sm is written
+      if (htid < 32) {
+        if (n_live && !n_is_v) na = *reinterpret_cast<const uint4*>(x_sm + 8 * nch);
+        uint16_t sc;
+        const uint32_t codes = i4_quantise8(na, sc);
+        if (n_live) {
+          const long long slot = p.ring_cap > 0 ? p.off % p.ring_cap : p.off;
+          const long long crow = (long long)bg * p.cap + slot;
+          reinterpret_cast<uint32_t*>(n_is_v ? p.cv : p.ck)[crow * CH + nch] = codes;
+          *reinterpret_cast<uint32_t*>(smem + (n_is_v ? C::OFF_XV : C::OFF_XK) + i4_off<D>(0, nch / 4) +
+                                       4 * (nch & 3)) = codes;
+          if ((nch & 3) == 0) {
+            reinterpret_cast<uint16_t*>(n_is_v ? p.cvs : p.cks)[crow * NB + nch / 4] = sc;
+            reinterpret_cast<uint16_t*>(smem + (n_is_v ? C::OFF_XVS : C::OFF_XS))[nch / 4] = sc;
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(row_bar);
+      }
+    };
+    uint32_t merge_phase = 0;
+    int end = min(u1, bg * per + per);
+    prepare(0, end == bg * per + per);
+    if (end == bg * per + per) put_row();
+    named_bar_sync(2, C::HELPERS);   // x_sm is read
+    for (int i = 0; end < u1; ++i) {
+      const int bg_i = bg, b_i = b, g_i = g, c0 = first_cta(), c1 = last_cta();
+      next_pair();
+      end = min(u1, bg * per + per);
+      prepare(i + 1, end == bg * per + per);
+      // pair i's partials, merged
+      if (!mbar_wait_asleep(part_bar, (uint32_t)(i & 1))) flag[0] = 1;
+      if (end == bg * per + per) put_row();
+      decode_finish<D, C, C::HELPERS, 2>(p, htid, red, smem + C::OFF_RED, C::RED_BYTES, merge_bar, merge_phase,
+                                         flag + 1, reinterpret_cast<const float*>(q_buf(i) + C::Q_SINK), g_i, b_i,
+                                         cta - c0, c1 - c0 + 1, p.ws_rec + (long long)(c0 + bg_i) * p.rec_floats);
+      named_bar_sync(2, C::HELPERS);   // all have read flag[1], the partials and x_sm
+      if (lane == 0) mbar_arrive(free_bar);
+    }
+    return;
   }
 
   // ---------------------------------------------------------------- consumers
@@ -647,64 +742,17 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
   uint32_t off[NB];   // this lane's ldmatrix row (row `lane` of the warp's) in a stage
 #pragma unroll
   for (int blk = 0; blk < NB; ++blk) off[blk] = i4_off<D>(32 * warp + lane, blk);
-  uint32_t merge_phase = 0, phase = 0;
-  int slot = 0;
-  for (int u = u0; u < u1;) {
+  uint32_t phase = 0;
+  int slot = 0, i = 0;
+  for (int u = u0;; ++i) {
     const int bg0 = bg * per;                       // the pair's first unit
     const int end = min(u1, bg0 + per);
     // the CTA with the pair's last unit attends the new row, in warp 0
-    const bool last_cta = end == bg0 + per, new_row = last_cta && warp == 0;
-    {
-      const float sink_in = (threadIdx.x < QM && p.sinks) ? p.sinks[g * QM + threadIdx.x] : -INFINITY;
-      if (warp < 3) {
-        uint4 x1 = make_uint4(0, 0, 0, 0), x2 = x1;
-        if (rot_in && (rot_row < QM || last_cta)) {
-          const __nv_bfloat16* src = rot_src();
-          x1 = *reinterpret_cast<const uint4*>(src);
-          x2 = *reinterpret_cast<const uint4*>(src + HALF);
-          if (p.rope) rotate8(x1, x2, ctab, stab);
-          if (rot_row == QM) {
-            *reinterpret_cast<uint4*>(x_sm + 8 * rot_ch) = x1;
-            *reinterpret_cast<uint4*>(x_sm + HALF + 8 * rot_ch) = x2;
-          }
-        }
-        const int row = min(rot_row, 7);   // lanes past the queries write nothing
-        const float hs = i4_query<D>(x1, x2, rot_row < QM ? rot_ch : 8, qw_sm + row * (D / 8), qsum_sm + row * (D / 8),
-                                     p.scale_log2);
-        if (rot_row < QM && rot_ch == 0) hs_sm[rot_row] = hs;
-      }
-      if (threadIdx.x < QM) sink_sm[threadIdx.x] = sink_in * 1.4426950408889634f;
-    }
-    // The new row, 8 elements a lane: lanes 0.. its K, lanes 16.. its V.
-    constexpr int CH = D / 8;
-    const int nch = lane & 15;                       // this lane's chunk
-    const bool n_live = new_row && nch < CH, n_is_v = lane >= 16;
-    uint4 na = make_uint4(0, 0, 0, 0);
-    if (n_live && n_is_v) na = *reinterpret_cast<const uint4*>(p.v + b * p.vs0 + (long long)g * p.vs2 + 8 * nch);
-    named_bar_sync(1, 32 * C::NCW);
+    const bool new_row = end == bg0 + per && warp == 0;
+    if (!mbar_wait(q_bar(i), (uint32_t)((i >> 1) & 1))) flag[0] = 1;
     I4State<D> z;
-    i4_start<D>(z, qw_sm, qsum_sm, hs_sm, QM, lane);
-    // Quantise it, write it to the cache and stage it in smem as row 0 of a
-    // tile (the other rows are masked).
-    if (new_row) {
-      if (n_live && !n_is_v) na = *reinterpret_cast<const uint4*>(x_sm + 8 * nch);
-      uint16_t sc;
-      const uint32_t codes = i4_quantise8(na, sc);
-      if (n_live) {
-        const long long slot = p.ring_cap > 0 ? p.off % p.ring_cap : p.off;
-        const long long crow = (long long)bg * p.cap + slot;
-        uint32_t* cc = reinterpret_cast<uint32_t*>(n_is_v ? p.cv : p.ck) + crow * CH + nch;
-        uint16_t* cs = reinterpret_cast<uint16_t*>(n_is_v ? p.cvs : p.cks) + crow * NB + nch / 4;
-        *cc = codes;
-        *reinterpret_cast<uint32_t*>(smem + (n_is_v ? C::OFF_XV : C::OFF_XK) + i4_off<D>(0, nch / 4) +
-                                     4 * (nch & 3)) = codes;
-        if ((nch & 3) == 0) {
-          *cs = sc;
-          reinterpret_cast<uint16_t*>(smem + (n_is_v ? C::OFF_XVS : C::OFF_XS))[nch / 4] = sc;
-        }
-      }
-      __syncwarp();
-    }
+    i4_start<D>(z, reinterpret_cast<const uint4*>(q_buf(i)), reinterpret_cast<const float*>(q_buf(i) + C::Q_SUM),
+                reinterpret_cast<const float*>(q_buf(i) + C::Q_HS), QM, lane);
 
     // The share's rows of this pair from position pos0 on: the first skip ones
     // lie before the band. left and skip count from this warp's rows of a stage.
@@ -723,6 +771,8 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
         kt = sbase + C::OFF_K + slot * C::STAGE_BYTES;
         ks = sbase + C::OFF_KS + slot * C::SC_BYTES + (uint32_t)(32 * warp * NB * 2);
       } else {
+        // (every pair of this CTA before this one ended here: use i of row_bar)
+        if (!mbar_wait(row_bar, (uint32_t)(i & 1))) { flag[0] = 1; break; }
         left = 1;
         skip = 0;
       }
@@ -743,27 +793,21 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
         }
       }
     }
+    if (i > 0 && !mbar_wait(free_bar, (uint32_t)((i - 1) & 1))) flag[0] = 1;   // the last pair's partials are read
     i4_write_partial<D>(z, reinterpret_cast<float*>(smem + C::OFF_RED) + warp * (C::RED_WARP / 4), lane);
-    named_bar_sync(1, 32 * C::NCW);
-
-    // The pair's CTAs. CTA c's record of pair bg is record c + bg of all: the
-    // shares' borders and the pairs' make one staircase.
-    const int c_first = p.S > 0 ? bg * p.S : holder(bg0);
-    const int c_last = p.S > 0 ? c_first + p.S - 1 : holder(bg0 + per - 1);
-    const bool idle = end == u1;   // the ring holds nothing to come: it takes the records
-    decode_finish<D, C>(p, reinterpret_cast<const float*>(smem + C::OFF_RED), smem + (idle ? 0u : C::OFF_RED),
-                        idle ? C::RING_BYTES : C::RED_BYTES, merge_bar, merge_phase, flag, sink_sm, g, b, cta - c_first,
-                        c_last - c_first + 1, p.ws_rec + (long long)(c_first + bg) * p.rec_floats);
     u = end;
-    if (u < u1) {
-      named_bar_sync(1, 32 * C::NCW);   // the partials, the sinks and flag[1] are free for the next pair
-      ++bg;
-      if (++g == p.n_kv) {
-        g = 0;
-        ++b;
-      }
-    }
+    if (u == u1) break;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(part_bar);
+    next_pair();
   }
+  named_bar_sync(1, 32 * C::NCW);
+  // The last pair. The ring holds nothing to come: it takes the records.
+  uint32_t merge_phase = 0;
+  const int c0 = first_cta();
+  decode_finish<D, C, 32 * C::NCW, 1>(p, threadIdx.x, red, smem, C::RING_BYTES, last_merge_bar, merge_phase, flag + 2,
+                                      reinterpret_cast<const float*>(q_buf(i) + C::Q_SINK), g, b, cta - c0,
+                                      last_cta() - c0 + 1, p.ws_rec + (long long)(c0 + bg) * p.rec_floats);
 }
 
 }  // namespace sa
