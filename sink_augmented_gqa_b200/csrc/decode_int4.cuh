@@ -29,8 +29,9 @@
 //   blocks, is one more product in bf16 (the scales as stored against the
 //   queries' sums in three bf16 parts) and what the fp32 sums start from.
 //   (m16n8k32 in e4m3 reads a byte 0000uuuu as u 2^-9 and needs half of the
-//   masks, but runs here as conversions and two f16 products: 219 us against
-//   the 166 of f16 at 16 sequences of 65,536 rows.)
+//   masks, but runs here as conversions and two f16 products and was no faster:
+//   166 us against 160 of f16 at 16 sequences of 65,536 rows, in an earlier form
+//   of this kernel.)
 // O^T += V^T P'^T, m16n8k16 in f16, P' = p * scale_v, transposed by movmatrix:
 //   ldmatrix.trans over 16-bit units hands a lane the same 4 codes of two
 //   neighbouring keys; x & 0x000F000F as f16 are the subnormals u 2^-24 of
@@ -747,8 +748,6 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
   for (int u = u0;; ++i) {
     const int bg0 = bg * per;                       // the pair's first unit
     const int end = min(u1, bg0 + per);
-    // the CTA with the pair's last unit attends the new row, in warp 0
-    const bool new_row = end == bg0 + per && warp == 0;
     if (!mbar_wait(q_bar(i), (uint32_t)((i >> 1) & 1))) flag[0] = 1;
     I4State<D> z;
     i4_start<D>(z, reinterpret_cast<const uint4*>(q_buf(i)), reinterpret_cast<const float*>(q_buf(i) + C::Q_SUM),
@@ -760,12 +759,18 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
     const long long pos0 = p.lo + (long long)k0 * C::UNIT;
     const int rows = (int)(min(p.off, p.lo + (long long)k_end * C::UNIT) - pos0);
     int left = rows - 32 * warp, skip = (int)max(p.lo_mask - pos0, 0LL) - 32 * warp;
-    // the stages, and for the warp with the new row its tile as one more
+    // The stages, and in the CTA with the pair's last unit one warp has the new
+    // row's tile as one more: the first that the last stage leaves idle, or where
+    // it is full each in its turn (one and the same held the others up: 74.4 us
+    // against 70.9 for 64 sequences of 8,192 rows, d = 64).
     const int n_st = (k_end - k0 + C::R / C::UNIT - 1) / (C::R / C::UNIT);
+    const int busy = ((rows + 31) / 32) % C::NCW;
+    const bool new_row = end == bg0 + per && warp == (busy > 0 ? busy : i % C::NCW);
     const int n_it = flag[0] ? 0 : n_st + (new_row ? 1 : 0);
     for (int j = 0; j < n_it; ++j) {
-      // the new row's tile stands to V's as a stage does
-      uint32_t kt = sbase + C::OFF_XK, ks = sbase + C::OFF_XS;
+      // the new row's tile stands to V's as a stage does (off counts from the
+      // stage's start: 32 rows are whole patterns of the swizzle)
+      uint32_t kt = sbase + C::OFF_XK - (uint32_t)(32 * warp * C::ROWB), ks = sbase + C::OFF_XS;
       if (j < n_st) {
         if (!mbar_wait(full_bar(slot), phase)) { flag[0] = 1; break; }
         kt = sbase + C::OFF_K + slot * C::STAGE_BYTES;
