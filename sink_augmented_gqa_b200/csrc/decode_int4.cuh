@@ -492,7 +492,8 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
   auto q_bar = [&](int i) -> uint32_t { return bar0 + 8u * (uint32_t)(2 * C::NS + (i & 1)); };
   const uint32_t part_bar = bar0 + 8u * (2 * C::NS + 2), free_bar = part_bar + 8, row_bar = part_bar + 16,
                  merge_bar = part_bar + 24, last_merge_bar = part_bar + 32;
-  // flag[0]: abort; flag[1], flag[2]: "this CTA merges the pair's records"
+  // flag[0]: a wait ran out, and no rows are brought or attended any more;
+  // flag[1], flag[2]: "this CTA merges the pair's records"
   volatile int* flag = reinterpret_cast<volatile int*>(smem + C::OFF_FLAG);
   const float* red = reinterpret_cast<const float*>(smem + C::OFF_RED);
   auto q_buf = [&](int i) -> uint8_t* { return smem + C::OFF_Q + (uint32_t)(i & 1) * C::Q_BYTES; };
@@ -653,10 +654,9 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
         u += units;
         if (k + units == per) next_pair();
       }
-      if (flag[0]) {
-        for (int j = (it > C::NS ? it - C::NS : 0); j < it; ++j)
-          mbar_wait_drain(full_bar(j % C::NS), (uint32_t)((j / C::NS) & 1));
-      }
+      // Copies still in flight keep this CTA, also when the consumers gave up.
+      for (int j = (it > C::NS ? it - C::NS : 0); j < it; ++j)
+        mbar_wait_drain(full_bar(j % C::NS), (uint32_t)((j / C::NS) & 1));
       return;
     }
     // ------------------------------------------------------------ helpers
@@ -746,9 +746,9 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
   uint32_t phase = 0;
   int slot = 0, i = 0;
   for (int u = u0;; ++i) {
-    const int bg0 = bg * per;                       // the pair's first unit
+    const int bg0 = u / per * per;   // the pair's first unit
     const int end = min(u1, bg0 + per);
-    if (!mbar_wait(q_bar(i), (uint32_t)((i >> 1) & 1))) flag[0] = 1;
+    if (!flag[0] && !mbar_wait(q_bar(i), (uint32_t)((i >> 1) & 1))) flag[0] = 1;
     I4State<D> z;
     i4_start<D>(z, reinterpret_cast<const uint4*>(q_buf(i)), reinterpret_cast<const float*>(q_buf(i) + C::Q_SUM),
                 reinterpret_cast<const float*>(q_buf(i) + C::Q_HS), QM, lane);
@@ -798,15 +798,18 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
         }
       }
     }
-    if (i > 0 && !mbar_wait(free_bar, (uint32_t)((i - 1) & 1))) flag[0] = 1;   // the last pair's partials are read
+    // the last pair's partials are read
+    if (i > 0 && !mbar_wait(free_bar, (uint32_t)((i - 1) & 1))) flag[0] = 1;
     i4_write_partial<D>(z, reinterpret_cast<float*>(smem + C::OFF_RED) + warp * (C::RED_WARP / 4), lane);
     u = end;
     if (u == u1) break;
     __syncwarp();
     if (lane == 0) mbar_arrive(part_bar);
-    next_pair();
   }
   named_bar_sync(1, 32 * C::NCW);
+  bg = (u1 - 1) / per;
+  b = bg / p.n_kv;
+  g = bg - b * p.n_kv;
   // The last pair. The ring holds nothing to come: it takes the records.
   uint32_t merge_phase = 0;
   const int c0 = first_cta();

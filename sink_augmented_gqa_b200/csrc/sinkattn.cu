@@ -585,8 +585,11 @@ struct DecodePlan {
   long long records;   // records in the workspace; 0: none is needed
 };
 
-// Units of 128 rows that taking up another (b, g) costs a CTA of an INT4 decode
-// (merging and the next queries take ~5 us, in which an SM attends 2,000 rows).
+// Units of 128 rows that taking up another (b, g), and the merge of one that
+// two CTAs share, cost a CTA of an INT4 decode. d = 64, 8 KV heads, dealt out
+// against equal shares: 12 sequences of 5,500 rows (15 units more for the
+// fullest CTA) 16.6 us against 19.0; 7 of 16,000 (also 15) 24.4 against 23.6;
+// 12 of 8,000 (22) equal shares 23.
 constexpr long long kI4Border = 16;
 
 DecodePlan plan_decode(const sa_kv_cache* c, const sa_attn_args* a) {

@@ -314,6 +314,93 @@ def _check_scaled(gpu, ref, what):
     assert err.max() <= 1e-2 and err.mean() <= 1e-3, f"{what}: max {err.max()} mean {err.mean()}"
 
 
+@pytest.mark.parametrize("over", [dict(B=40, n_q=16, n_kv=8, d=64), dict(B=37, n_q=35, n_kv=5, d=96),
+                                  dict(B=75, n_q=8, n_kv=4, d=128), dict(B=10, n_q=64, n_kv=8, d=64)],
+                         ids=["d64", "d96", "d128", "gptoss"])
+@pytest.mark.parametrize("window", [0, 200], ids=["full", "band"])
+@pytest.mark.parametrize("off", [0, 130, 777, 2048, 6001])
+def test_decode_of_many_pairs(cuda_device, over, window, off):
+    # more (sequence, KV head) pairs than SMs, or long ones that do not divide
+    # into them: CTAs end one pair, span some and begin another
+    if off == 6001 and over["B"] != 10:
+        off = 1200
+    cfg, cache, oracle, cos, sin = _setup(over, "int4", off, 2)
+    ws = sa.decode_workspace(cfg.B, cfg.n_q, cfg.n_kv, cfg.d, device=DEV)
+    sinks = wl.sinks(cfg)
+    for step in range(2):
+        _decode(cfg, cache, oracle, cos, sin, window, sinks, step + 1, ws, f"int4 decode {step}")
+    assert torch.count_nonzero(ws[: 8 * cfg.B * cfg.n_kv]) == 0
+
+
+def test_decode_of_many_pairs_on_a_ring(cuda_device):
+    cfg, cache, oracle, cos, sin = _setup(dict(B=40, n_q=16, n_kv=8, d=64), "int4", 1200, 4, ring_window=300)
+    sinks = wl.sinks(cfg)
+    for step in range(3):
+        _decode(cfg, cache, oracle, cos, sin, 300, sinks, step + 1, None, f"ring decode {step}")
+
+
+def test_decode_graphs_that_share_a_workspace(cuda_device):
+    # two layers' calls captured into two graphs over one workspace, replayed in turn
+    over = dict(B=2, n_q=16, n_kv=2, d=64)
+    ws = sa.decode_workspace(2, 16, 2, 64, device=DEV)
+    made = []
+    stream = torch.cuda.Stream()
+    for window in (0, 128):
+        cfg, cache, oracle, cos, sin = _setup(over, "int4", 2500, 1, seed=window)
+        q, k, v = wl.qkv(cfg, 1, step=1)
+        ref, ref_lse, _ = oracle.call(q, k, v, None, window)
+        q, k, v = (t.to(DEV) for t in (q, k, v))
+        out = torch.empty_like(q)
+        stream.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            sa.attn_decode(cache, q, k, v, None, window, cfg.sm_scale, cos, sin, workspace=ws, out=out)
+        made.append((graph, out, ref, cache, q, k, v, cos, sin))
+    for _ in range(3):
+        for graph, out, *_ in made:
+            out.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, ref, *_ in made:
+            check_bf16_output(out, ref, "replayed in turn")
+
+
+@pytest.mark.parametrize("over,off", [(dict(B=2, n_q=8, n_kv=2, d=64), 3000), (dict(B=40, n_q=16, n_kv=8, d=64), 700),
+                                      (dict(B=1, n_q=8, n_kv=1, d=64), 40000)])
+def test_zero_wait_limit_is_right_or_reported(cuda_device, over, off):
+    cfg, cache, oracle, cos, sin = _setup(over, "int4", off, 40)
+    ws = sa.decode_workspace(cfg.B, cfg.n_q, cfg.n_kv, cfg.d, device=DEV)
+    q, k, v = (t.to(DEV) for t in wl.qkv(cfg, 1, step=1))
+    q2, k2, v2 = (t.to(DEV) for t in wl.qkv(cfg, 20, step=2))
+    snap, osnap = cache.snapshot(), oracle.cache.snapshot()
+    ref = oracle.call(q, k, v, None, 0)[0]
+    oracle.cache.restore(osnap)
+    torch.cuda.synchronize()
+    assert sa.device_status() == "SA_OK"
+    sa.set_wait_limit(0)
+    try:
+        out = sa.attn_decode(cache, q, k, v, None, 0, cfg.sm_scale, cos, sin, workspace=ws)
+        torch.cuda.synchronize()
+        decode_status = sa.device_status()
+        sa.attn_prefill_quant(cache, q2, k2, v2, None, 0, cfg.sm_scale, cos, sin)
+        torch.cuda.synchronize()
+        prefill_status = sa.device_status()
+        print("zero wait limit:", decode_status, prefill_status)
+    finally:
+        sa.set_wait_limit(2_000_000_000)
+    # A wait asks at least once, and the hardware holds that for a moment: what
+    # arrives meanwhile is no timeout, and the answer is then right.
+    assert {decode_status, prefill_status} <= {"SA_OK", "SA_ERR_TIMEOUT"}
+    if decode_status == "SA_OK":
+        check_bf16_output(out, ref, "without a limit")
+    # the tickets are where they were, and the calls after it are right
+    assert torch.count_nonzero(ws[: 8 * cfg.B * cfg.n_kv]) == 0
+    cache.restore(snap)
+    for step in range(2):
+        _decode(cfg, cache, oracle, cos, sin, 0, None, step + 1, ws, "after timeout")
+    assert sa.device_status() == "SA_OK"
+
+
 @pytest.mark.parametrize("window", [0, 128], ids=["full", "band"])
 def test_decode_mixed_magnitude_rows(cuda_device, window):
     # K of normal size, V rows from 1e-37 to 1e30 next to one another
