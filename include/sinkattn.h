@@ -341,7 +341,8 @@ sa_status sa_attn_prefill(sa_kv_cache* cache, const sa_attn_args* args, sa_strea
  *   bf16 (reading them back once costs a fraction of the attention over them
  *   for all heads and rows). Calls that share a workspace must not overlap on
  *   the device; it may be shared by all layers of a model.
- * `out` may be `q` itself but must not overlap the workspace otherwise.
+ * `out` may be `q` itself; else it overlaps no input, the cache nor the
+ * workspace.
  * Schedule counters and graph capture as for sa_attn_prefill.
  * SA_ERR_UNSUPPORTED on a bf16 cache (sa_attn_prefill); SA_ERR_WORKSPACE.
  */
@@ -365,7 +366,7 @@ size_t sa_attn_prefill_quant_workspace_size(const sa_kv_cache* cache, int32_t T,
  * product as f16. On an INT4 cache the new row is likewise stored and
  * attended quantised; codes enter both products as integers, queries the QK
  * product in f16 after an exact per-head power-of-two scaling, the weights
- * times the block scales of V the PV product as bf16.
+ * times the block scales of V the PV product as f16.
  * The rows are shared out among the CTAs of each (sequence, KV head) at run
  * time (the CTAs that stream faster take more), so the fp32 partial sums are
  * grouped differently from call to call: two identical calls can differ in

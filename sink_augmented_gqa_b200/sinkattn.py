@@ -171,8 +171,11 @@ def _stream(t=None):
 
 
 def _raw_stream(t):
-    """The current stream of t's device as a raw handle (no Stream object)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index)
+    """The current stream of t's device, which must be the current one, as a raw handle (no Stream object)."""
+    index = t.device.index
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _ptr(t):
@@ -313,6 +316,9 @@ class KVCache:
     def append(self, k_rot, v):
         """kv_append: copy already-rotated k and v rows at [offset, offset + T)."""
         ks, vs = _view4("k_rot", k_rot), _view4("v", v)
+        raw, shape = self.raw, k_rot.shape
+        if v.shape != shape or shape != (raw.B, shape[1], raw.n_kv, raw.d):
+            raise ValueError("k_rot and v must be [B, T, n_kv, d] with the cache's B, n_kv and d")
         _check(lib().sa_kv_append(ctypes.byref(self.raw), k_rot.data_ptr(), _I64x3(ks[0], ks[1], ks[2]), v.data_ptr(),
                                   _I64x3(vs[0], vs[1], vs[2]), k_rot.shape[1], _raw_stream(self.k)), "sa_kv_append")
 
@@ -362,6 +368,10 @@ def _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, ls
     """sa_attn_args for one call, packed into this thread's reusable struct
     (the library reads it only during the call)."""
     qs, ks, vs, os_ = _view4("q", q), _view4("k", k), _view4("v", v), _view4("out", out)
+    shape, kv = q.shape, k.shape
+    if v.shape != kv or out.shape != shape or kv != (shape[0], shape[1], cache.raw.n_kv, shape[3]) \
+            or shape[3] != cache.raw.d:
+        raise ValueError("k and v must be [B, T, n_kv, d] and out like q, with the cache's n_kv and d")
     if sinks is not None and (sinks.dtype != torch.float32 or not sinks.is_contiguous()):
         raise TypeError("sinks must be a contiguous fp32 CUDA tensor")
     a = getattr(_tls, "args", None)
@@ -404,6 +414,8 @@ def attn_prefill_quant(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=No
     B, T, n_q, d = q.shape
     if workspace is None:
         workspace = prefill_quant_workspace(cache, T, window)
+    elif not (workspace.is_cuda and workspace.is_contiguous()):
+        raise TypeError("workspace must be a contiguous CUDA tensor")
     if out is None:
         out = _empty4(B, T, n_q, d, q.device)
     if return_lse and lse is None:

@@ -3,8 +3,10 @@ read-back and prefill on quantised caches reject bad arguments on the host
 before any launch, and leave the cache's state alone."""
 
 import ctypes
+from types import SimpleNamespace
 
 import pytest
+import torch
 
 from sink_augmented_gqa_b200 import build as sbuild
 from sink_augmented_gqa_b200 import sinkattn as S
@@ -144,3 +146,34 @@ def test_binding_checks():
         c.read(5, 4)
     with pytest.raises(AssertionError):
         S.KVCache(1, 96, 2, 64, device="cpu", int4=True, k_scale=c.k_scale.float())
+
+
+def test_binding_refuses_other_shapes_and_devices(monkeypatch):
+    """What the C side cannot see from pointers and strides: shapes that do
+    not fit the cache, and tensors of a device that is not the current one."""
+    monkeypatch.setattr(S, "_view4", lambda name, t: t.stride())    # CPU tensors stand in: nothing is launched
+    c = S.KVCache(2, 96, 2, 64, device="cpu", int4=True)
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)             # noqa: E731
+    for k, v in ((z(2, 3, 2, 64), z(2, 4, 2, 64)), (z(1, 3, 2, 64), z(1, 3, 2, 64)), (z(2, 3, 4, 64), z(2, 3, 4, 64)),
+                 (z(2, 3, 2, 96), z(2, 3, 2, 96))):
+        with pytest.raises(ValueError):
+            c.append(k, v)
+    q, kv = z(2, 3, 8, 64), z(2, 3, 2, 64)
+    ws = torch.zeros(1 << 16, dtype=torch.uint8)
+    for args in ((q, kv, z(2, 4, 2, 64)), (q, z(2, 2, 2, 64), z(2, 2, 2, 64)), (q, z(2, 3, 4, 64), z(2, 3, 4, 64)),
+                 (z(2, 3, 8, 96), z(2, 3, 2, 96), z(2, 3, 2, 96))):
+        with pytest.raises(ValueError):
+            S.attn_prefill_quant(c, *args, None, 0, 0.125, rope_fused=False)
+        with pytest.raises(ValueError):
+            S.attn_decode(c, *args, None, 0, 0.125, rope_fused=False, workspace=ws)
+    with pytest.raises(ValueError):
+        S.attn_prefill_quant(c, q, kv, kv, None, 0, 0.125, rope_fused=False, out=z(2, 2, 8, 64))
+    with pytest.raises(TypeError):                                   # a workspace in host memory
+        S.attn_prefill_quant(c, q, kv, kv, None, 0, 0.125, rope_fused=False, workspace=ws)
+    assert c.offset == 0
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 7, raising=False)
+    at = lambda i: SimpleNamespace(device=SimpleNamespace(index=i))  # noqa: E731
+    assert S._raw_stream(at(0)) == 7
+    with pytest.raises(ValueError):
+        S._raw_stream(at(1))

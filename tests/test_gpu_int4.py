@@ -365,6 +365,20 @@ def test_decode_graphs_that_share_a_workspace(cuda_device):
             check_bf16_output(out, ref, "replayed in turn")
 
 
+def test_decode_static_refuses_what_its_scratch_cannot_hold(cuda_device):
+    # 240 pairs in equal shares: a record of 4 KB for each of the CTAs and borders, over a MiB
+    cfg, cache, oracle, cos, sin = _setup(dict(B=30, n_q=64, n_kv=8, d=128), "int4", 600, 2)
+    q, k, v = (t.to(DEV) for t in wl.qkv(cfg, 1, step=1))
+    with pytest.raises(sa.SinkAttnError) as e:
+        sa.attn_decode_static(cache, q, k, v, None, 0, cfg.sm_scale, cos, sin)
+    assert e.value.name == "SA_ERR_WORKSPACE" and cache.offset == 600
+    ws = sa.decode_workspace(cfg.B, cfg.n_q, cfg.n_kv, cfg.d, device=DEV)
+    with pytest.raises(sa.SinkAttnError) as e:
+        sa.attn_decode(cache, q, k, v, None, 0, cfg.sm_scale, cos, sin, workspace=ws[:1 << 20])
+    assert e.value.name == "SA_ERR_WORKSPACE" and cache.offset == 600
+    _decode(cfg, cache, oracle, cos, sin, 0, None, 1, ws, "with a workspace")
+
+
 @pytest.mark.parametrize("over,off", [(dict(B=2, n_q=8, n_kv=2, d=64), 3000), (dict(B=40, n_q=16, n_kv=8, d=64), 700),
                                       (dict(B=1, n_q=8, n_kv=1, d=64), 40000)])
 def test_zero_wait_limit_is_right_or_reported(cuda_device, over, off):
