@@ -368,9 +368,8 @@ def _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, ls
     """sa_attn_args for one call, packed into this thread's reusable struct
     (the library reads it only during the call)."""
     qs, ks, vs, os_ = _view4("q", q), _view4("k", k), _view4("v", v), _view4("out", out)
-    shape, kv = q.shape, k.shape
-    if v.shape != kv or out.shape != shape or kv != (shape[0], shape[1], cache.raw.n_kv, shape[3]) \
-            or shape[3] != cache.raw.d:
+    raw, shape, kv = cache.raw, q.shape, k.shape
+    if v.shape != kv or out.shape != shape or kv != (shape[0], shape[1], raw.n_kv, shape[3]) or shape[3] != raw.d:
         raise ValueError("k and v must be [B, T, n_kv, d] and out like q, with the cache's n_kv and d")
     if sinks is not None and (sinks.dtype != torch.float32 or not sinks.is_contiguous()):
         raise TypeError("sinks must be a contiguous fp32 CUDA tensor")
@@ -380,7 +379,7 @@ def _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, ls
     struct.pack_into(_ATTN_FMT, a, 0,
                      q.data_ptr(), qs[0], qs[1], qs[2], k.data_ptr(), ks[0], ks[1], ks[2],
                      v.data_ptr(), vs[0], vs[1], vs[2], 0 if sinks is None else sinks.data_ptr(),
-                     q.shape[0], q.shape[1], q.shape[2], cache.raw.offset, int(window), float(sm_scale),
+                     shape[0], shape[1], shape[2], raw.offset, int(window), float(sm_scale),
                      1 if rope_fused else 0, 0 if cos is None else cos.data_ptr(),
                      0 if sin is None else sin.data_ptr(), 0 if cos is None else cos.shape[0],
                      out.data_ptr(), os_[0], os_[1], os_[2], 0 if lse is None else lse.data_ptr())
