@@ -339,7 +339,8 @@ sa_status sa_attn_prefill(sa_kv_cache* cache, const sa_attn_args* args, sa_strea
  * workspace: device memory of sa_attn_prefill_quant_workspace_size() bytes,
  *   16-byte aligned, contents irrelevant: the rows that the call attends as
  *   bf16 (reading them back once costs a fraction of the attention over them
- *   for all heads and rows). Calls that share a workspace must not overlap on
+ *   for all heads and rows), and partial sums where a call has too few rows
+ *   and heads to give every SM work and its keys are shared out. Calls that share a workspace must not overlap on
  *   the device; it may be shared by all layers of a model.
  * `out` may be `q` itself; else it overlaps no input, the cache nor the
  * workspace.
@@ -351,7 +352,9 @@ sa_status sa_attn_prefill_quant(sa_kv_cache* cache, const sa_attn_args* args, vo
 
 /* Workspace bytes of sa_attn_prefill_quant for T rows at the cache's present
  * offset: K and V of T + (window > 0 ? min(offset, window - 1) : offset)
- * positions in bf16. 0 for an invalid cache or T < 1. */
+ * positions in bf16, and where those are long enough to be shared out (four
+ * key tiles, of 128, 96 or 64 keys for d = 64, 96, 128) 160 * 256 fp32 rows of
+ * d + 2. 0 for an invalid cache or T < 1. */
 size_t sa_attn_prefill_quant_workspace_size(const sa_kv_cache* cache, int32_t T, int32_t window);
 
 /*

@@ -63,6 +63,12 @@ struct PrefillParams {
   int n_pairs;
   int sched_slot;   // which counter pair of g_prefill_sched this launch uses
   int ring_cap;     // 0: cache row = position; > 0: ring cache, row = position mod ring_cap
+  // The PARTS kernels only:
+  int pack;         // query heads per tile: 1, or q_mult (row m tpos + t of a tile: head m, position t)
+  int tpos;         // positions per tile: 128 / pack
+  int splits;       // parts an item's key tiles are cut into, each an item of its own; > 1: partials
+  float2* part_ml;  // [item][256 rows] (running max in log2 units, sum)
+  float* part_o;    // [item][256 rows][d], relative to that max
 };
 
 // Work counters of the dynamic item schedule, one pair per launch slot (the
@@ -163,34 +169,38 @@ __device__ __forceinline__ int floordiv(int a, int b) {  // b > 0
 //   full tiles    [f_lo[X], f_hi[X]): every key of the tile is admitted for all
 //                 128 rows (0 <= key <= p, and key > p - W on band layers), so
 //                 no mask is applied there.
-template <int BN>
+template <int BN, bool PARTS>
 struct TileGeom {
   int off;
+  int tpos;        // PARTS: positions per query tile, else 128
   int T, window;
   int i0;          // first query row of tile A
   int base;        // first key of key tile 0
   int ntiles;
   int a_lo[2], a_hi[2], f_lo[2], f_hi[2];
-  __device__ __forceinline__ bool valid(int X) const { return i0 + 128 * X < T; }
+  __device__ __forceinline__ int tp() const { return PARTS ? tpos : 128; }
+  __device__ __forceinline__ bool valid(int X) const { return i0 + tp() * X < T; }
   __device__ __forceinline__ int lo(int X) const {
-    const int p0 = off + i0 + 128 * X;
+    const int p0 = off + i0 + tp() * X;
     return window > 0 ? (p0 - window + 1 > 0 ? p0 - window + 1 : 0) : 0;
   }
   __device__ __forceinline__ int hi(int X) const {  // exclusive
-    const int last = min(T, i0 + 128 * X + 128);
+    const int last = min(T, i0 + tp() * X + tp());
     return off + last;
   }
   __device__ __forceinline__ bool active(int X, int t) const { return t >= a_lo[X] && t < a_hi[X]; }
   __device__ __forceinline__ bool full(int X, int t) const { return t >= f_lo[X] && t < f_hi[X]; }
 };
 
-template <int BN>
-__device__ __forceinline__ TileGeom<BN> make_geom(const PrefillParams& p, int pair) {
-  TileGeom<BN> g;
+// part: with PARTS, which of p.splits parts of the key tiles.
+template <int BN, bool PARTS>
+__device__ __forceinline__ TileGeom<BN, PARTS> make_geom(const PrefillParams& p, int pair, int part) {
+  TileGeom<BN, PARTS> g;
   g.off = (int)p.off;
+  g.tpos = p.tpos;
   g.T = p.T;
   g.window = p.window;
-  g.i0 = pair * 256;
+  g.i0 = pair * 2 * g.tp();
   const int diag = g.off + g.i0;
   const int loA = g.lo(0);
   if (p.ring_cap > 0) {
@@ -201,7 +211,7 @@ __device__ __forceinline__ TileGeom<BN> make_geom(const PrefillParams& p, int pa
     const int nb = (diag - loA + BN - 1) / BN;
     g.base = diag - BN * nb;
   }
-  const int hi = g.off + min(p.T, g.i0 + 256);
+  const int hi = g.off + min(p.T, g.i0 + 2 * g.tp());
   g.ntiles = (hi - g.base + BN - 1) / BN;
 #pragma unroll
   for (int X = 0; X < 2; ++X) {
@@ -215,15 +225,27 @@ __device__ __forceinline__ TileGeom<BN> make_geom(const PrefillParams& p, int pa
     g.a_lo[X] = alo < 0 ? 0 : alo;
     g.a_hi[X] = ahi > g.ntiles ? g.ntiles : ahi;
     // full: klo >= 0, klo + BN - 1 <= p0, and (band) klo > p0 + 127 - W
-    const int p0 = g.off + g.i0 + 128 * X;
+    const int p0 = g.off + g.i0 + g.tp() * X;
     int flo = floordiv(-g.base + BN - 1, BN);
     if (p.window > 0) {
-      const int w = floordiv(p0 + 127 - p.window - g.base, BN) + 1;
+      const int w = floordiv(p0 + g.tp() - 1 - p.window - g.base, BN) + 1;
       if (w > flo) flo = w;
     }
     const int fhi = floordiv(p0 - BN + 1 - g.base, BN) + 1;
     g.f_lo[X] = flo < g.a_lo[X] ? g.a_lo[X] : (flo > g.a_hi[X] ? g.a_hi[X] : flo);
     g.f_hi[X] = fhi > g.a_hi[X] ? g.a_hi[X] : (fhi < g.f_lo[X] ? g.f_lo[X] : fhi);
+  }
+  if (PARTS && p.splits > 1) {
+    const int t0 = (int)((long long)g.ntiles * part / p.splits);
+    g.ntiles = (int)((long long)g.ntiles * (part + 1) / p.splits) - t0;
+    g.base += BN * t0;
+#pragma unroll
+    for (int X = 0; X < 2; ++X) {
+      g.a_lo[X] = min(max(g.a_lo[X] - t0, 0), g.ntiles);
+      g.a_hi[X] = min(max(g.a_hi[X] - t0, 0), g.ntiles);
+      g.f_lo[X] = min(max(g.f_lo[X] - t0, 0), g.ntiles);
+      g.f_hi[X] = min(max(g.f_hi[X] - t0, 0), g.ntiles);
+    }
   }
   return g;
 }
@@ -254,8 +276,12 @@ __device__ __forceinline__ void issue_pv(uint32_t o_tmem, uint32_t p_tmem, uint6
            (accumulate || kk > 0) ? 1u : 0u);
 }
 
-// FINE: the polynomial exponentials to fp32 (exp2_fma2_fine).
-template <int D, bool FINE>
+// FINE: the polynomial exponentials to fp32 (exp2_fma2_fine). PARTS: a tile may
+// hold the query heads of a KV group side by side (pack), and an item's key
+// tiles may be cut into parts (splits) whose unnormalised partials
+// prefill_merge_kernel joins. (Kernels of their own: the same code without them
+// loses 4 % to the registers they take.)
+template <int D, bool FINE, bool PARTS = false>
 __global__ void __launch_bounds__(384, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -275,10 +301,11 @@ __global__ void __launch_bounds__(384, 1)
   const int lane = threadIdx.x & 31;
   ItemSchedule sched;
   sched.G = gridDim.x;
-  sched.per_pair = p.n_q * p.B;
+  sched.n_q = PARTS ? p.n_q / p.pack : p.n_q;
+  sched.per_pair = sched.n_q * p.B;
   sched.n_pairs = p.n_pairs;
-  sched.n_items = p.n_pairs * sched.per_pair;
-  sched.n_q = p.n_q;
+  sched.n_items = p.n_pairs * sched.per_pair * (PARTS ? p.splits : 1);
+  auto part_of = [&](int item) -> int { return PARTS ? item % p.splits : 0; };
   volatile int4* ring_item = reinterpret_cast<volatile int4*>(smem + C::OFF_BAR + 8 * BAR_IRING);
   volatile float* ring_sink = reinterpret_cast<volatile float*>(smem + C::OFF_BAR + 8 * BAR_IRING + 64);
   // Read item k of this CTA from the ring (all roles, in order): its id,
@@ -368,8 +395,8 @@ __global__ void __launch_bounds__(384, 1)
         float sink = -INFINITY;
         if (item < sched.n_items) {
           next = sched.G + atomicAdd(ctr, 1);   // the following item, fetched one ahead
-          sched.coords(item, pair, h, b);
-          if (p.sinks) sink = p.sinks[h];
+          sched.coords(PARTS ? item / p.splits : item, pair, h, b);
+          if (!PARTS && p.sinks) sink = p.sinks[h];
         }
         ring_item[sl].x = item;
         ring_item[sl].y = pair;
@@ -379,8 +406,8 @@ __global__ void __launch_bounds__(384, 1)
         mbar_arrive(bar(BAR_IFULL + sl));   // release: the ring entry is visible to acquirers
         if (item >= sched.n_items) break;
         const int rr = k;
-        const int g = h / p.q_mult;
-        const TileGeom<BN> geo = make_geom<BN>(p, pair);
+        const int g = PARTS ? h * p.pack / p.q_mult : h / p.q_mult;
+        const TileGeom<BN, PARTS> geo = make_geom<BN, PARTS>(p, pair, part_of(item));
         const int qb = j & 1;
         if (j >= 2 && !mbar_wait(bar(BAR_QEMPTY + qb), (uint32_t)(((j >> 1) - 1) & 1))) {
           *abort_flag = 1;
@@ -389,14 +416,15 @@ __global__ void __launch_bounds__(384, 1)
         // pipeline X takes row tile X ^ sw (see ItemSchedule::swap)
         const int sw = ItemSchedule::swap(rr);
         const int nq = geo.valid(1) ? 2 : 1;
-        mbar_arrive_expect_tx(bar(BAR_QFULL + qb), (uint32_t)nq * C::Q_BYTES);
+        mbar_arrive_expect_tx(bar(BAR_QFULL + qb),
+                              (uint32_t)nq * (PARTS ? (uint32_t)(p.pack * p.tpos) * D * 2 : C::Q_BYTES));
         for (int X = 0; X < 2; ++X) {
           const int rt = X ^ sw;
           if (!geo.valid(rt)) continue;
 #pragma unroll
           for (int cb = 0; cb < C::NCB; ++cb)
             tma_load_4d(sbase + C::OFF_Q + (2 * qb + X) * C::Q_BYTES + cb * C::QBLOCK, &tmQ,
-                        bar(BAR_QFULL + qb), cb * C::CB, geo.i0 + 128 * rt, h, b);
+                        bar(BAR_QFULL + qb), cb * C::CB, geo.i0 + geo.tp() * rt, PARTS ? h * p.pack : h, b);
         }
         ++j;
         for (int t = 0; t < geo.ntiles; ++t, ++gt) {
@@ -446,7 +474,7 @@ __global__ void __launch_bounds__(384, 1)
         int pair, h, b;
         const int item = fetch(rr, true, pair, h, b, sink_unused);
         if (item >= sched.n_items) break;
-        const TileGeom<BN> geo = make_geom<BN>(p, pair);
+        const TileGeom<BN, PARTS> geo = make_geom<BN, PARTS>(p, pair, part_of(item));
         const int sw = ItemSchedule::swap(rr);
 #pragma unroll
         for (int X = 0; X < 2; ++X) {
@@ -459,7 +487,8 @@ __global__ void __launch_bounds__(384, 1)
           const uint32_t stage = sbase + C::OFF_Q + (2 * (j & 1) + X) * C::Q_BYTES;
 #pragma unroll
           for (int cb = 0; cb < C::NCB; ++cb)
-            tma_store_4d(&tmO, stage + cb * C::QBLOCK, cb * C::CB, geo.i0 + 128 * rt, h, b);
+            if (!PARTS || p.splits == 1)
+              tma_store_4d(&tmO, stage + cb * C::QBLOCK, cb * C::CB, geo.i0 + geo.tp() * rt, PARTS ? h * p.pack : h, b);
           bulk_commit();
         }
         if (!ok) break;
@@ -492,7 +521,7 @@ __global__ void __launch_bounds__(384, 1)
         int pair, h, b;
         const int item = fetch(rr, true, pair, h, b, sink_unused);
         if (item >= sched.n_items) break;
-        const TileGeom<BN> geo = make_geom<BN>(p, pair);
+        const TileGeom<BN, PARTS> geo = make_geom<BN, PARTS>(p, pair, part_of(item));
         const int qb = j & 1;
         if (!mbar_wait(bar(BAR_QFULL + qb), (uint32_t)((j >> 1) & 1))) { ok = false; break; }
         tc_fence_after();
@@ -562,15 +591,23 @@ __global__ void __launch_bounds__(384, 1)
     int ntot = 0;   // cumulative key tiles of this query tile slot (S / P / O-done phases)
     int j = 0;      // items of this CTA so far (Q buffer j & 1 stages this item's output)
     bool ok = true;
+    // this thread's head and position within a tile (PARTS; rows behind the packed ones idle)
+    const int row_m = PARTS && p.pack > 1 ? r / p.tpos : 0, row_t = PARTS ? r - row_m * p.tpos : r;
     for (int rr = 0; ok; ++rr) {
       float sink_raw;
       int pair, h, b;
       const int item = fetch(rr, lane == 0, pair, h, b, sink_raw);
       if (item >= sched.n_items) break;
-      const TileGeom<BN> geo = make_geom<BN>(p, pair);
+      const int part = part_of(item);
+      const TileGeom<BN, PARTS> geo = make_geom<BN, PARTS>(p, pair, part);
       const int rt = X ^ ItemSchedule::swap(rr);   // row tile of this pipeline
-      const int i = geo.i0 + 128 * rt + r;      // query row within the call
-      const bool row_ok = i < p.T;
+      const int i = geo.i0 + geo.tp() * rt + row_t;      // query row within the call
+      bool row_ok = i < p.T;
+      if (PARTS) {
+        row_ok = row_ok && row_m < p.pack;
+        h = h * p.pack + row_m;
+        sink_raw = p.sinks && part == 0 && row_ok ? p.sinks[h] : -INFINITY;
+      }
       const long long pos = p.off + i;
       if (geo.valid(rt)) {
         const float sink2 = sink_raw * LOG2E;   // -inf without sinks
@@ -598,7 +635,7 @@ __global__ void __launch_bounds__(384, 1)
             // per column, skipped when no row of the tile needs it.
             // Positions fit in 32 bits (cap < 2^31).
             const int klo = geo.base + BN * t;
-            const int p0 = (int)p.off + geo.i0 + 128 * rt;   // position of row 0
+            const int p0 = (int)p.off + geo.i0 + geo.tp() * rt;   // position of row 0
             const int ipos = (int)pos;
             if (klo + BN - 1 > p0) {
               const int cmax = min(max(ipos - klo, -1), BN);
@@ -606,7 +643,7 @@ __global__ void __launch_bounds__(384, 1)
               for (int c = 0; c < BN; ++c)
                 if (c > cmax) sr[c] = __float_as_uint(-INFINITY);
             }
-            const int lo_last = p.window > 0 ? max(p0 + 128 - p.window, 0) : 0;   // lowest key of row 127
+            const int lo_last = p.window > 0 ? max(p0 + geo.tp() - p.window, 0) : 0;   // lowest key of the last row
             if (klo < lo_last) {
               const int lo_k = p.window > 0 ? max(ipos - p.window + 1, 0) : 0;
               const int cmin = min(max(lo_k - klo, 0), BN);
@@ -700,7 +737,32 @@ __global__ void __launch_bounds__(384, 1)
         // read, so the tile is free), then one TMA store of the 128 x d tile
         // (rows past T are dropped by the tensor map's bounds).
         uint8_t* stage = smem + C::OFF_Q + (2 * (j & 1) + X) * C::Q_BYTES;
-        if (ok && n > 0 && mbar_wait(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1)) && !*abort_flag) {
+        if (PARTS && p.splits > 1) {
+          // a part: O, the max and the sum as they are
+          const long long at = (long long)item * 256 + 128 * rt + r;
+          if (ok && n > 0 && mbar_wait(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1)) && !*abort_flag) {
+            tc_fence_after();
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 32) {
+              uint32_t o32[32];
+              tmem_ld32(o_tm + c0, o32);
+              tmem_wait_ld();
+              if (row_ok) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4)
+                  *reinterpret_cast<uint4*>(p.part_o + at * D + c0 + c) =
+                      make_uint4(o32[c], o32[c + 1], o32[c + 2], o32[c + 3]);
+              }
+            }
+          } else if (!ok || *abort_flag) {
+            ok = false;
+            *abort_flag = 1;
+          } else if (row_ok) {   // a part without keys for this tile
+            for (int c = 0; c < D; c += 4)
+              *reinterpret_cast<uint4*>(p.part_o + at * D + c) = make_uint4(0, 0, 0, 0);
+          }
+          if (row_ok) p.part_ml[at] = make_float2(m, l);
+        } else if (ok && n > 0 && mbar_wait(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1)) && !*abort_flag) {
           tc_fence_after();
           const float inv_l = 1.0f / l;
 #pragma unroll
@@ -755,6 +817,42 @@ __global__ void __launch_bounds__(384, 1)
       __threadfence();
     }
   }
+}
+
+// Joins the parts of prefill_kernel<D, true, true>: a row's D / 4 lanes sum its
+// partials relative to their largest max (the sink is in part 0) and write the
+// row and its lse. Its reads, 4 (d + 2) bytes a row and part, come from L2.
+template <int D>
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
+  constexpr int LANES = D / 4, RB = 256 / LANES;
+  const int rb = threadIdx.x / LANES, ch = threadIdx.x - rb * LANES;
+  const long long n = (long long)p.B * p.T * p.n_q, at = (long long)blockIdx.x * RB + rb;
+  if (rb >= RB || at >= n) return;
+  const int h = (int)(at % p.n_q), b = (int)(at / p.n_q / p.T), i = (int)(at / p.n_q % p.T);
+  const int hi = h / p.pack, m_i = h - hi * p.pack, pair = i / (2 * p.tpos), rest = i - pair * 2 * p.tpos;
+  const int rt = rest / p.tpos, t = rest - rt * p.tpos;
+  const int heads = p.n_q / p.pack;
+  const long long item = ((long long)(p.n_pairs - 1 - pair) * heads * p.B + (long long)b * heads + hi) * p.splits;
+  const long long row = item * 256 + 128 * rt + m_i * p.tpos + t;   // of part 0; the next ones 256 rows on
+  float M = -INFINITY;
+  for (int k = 0; k < p.splits; ++k) M = fmaxf(M, p.part_ml[row + 256LL * k].x);
+  float L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < p.splits; ++k) {
+    const float2 ml = p.part_ml[row + 256LL * k];
+    const float w = ex2(ml.x - M);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (row + 256LL * k) * D + 4 * ch);
+    L = fmaf(w, ml.y, L);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+  const float inv = 1.0f / L;
+  *reinterpret_cast<uint2*>(p.out + b * p.os0 + i * p.os1 + h * p.os2 + 4 * ch) =
+      make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  if (ch == 0 && p.lse) p.lse[((long long)b * p.n_q + h) * p.T + i] = (M + __log2f(L)) * 0.6931471805599453f;
 }
 
 }  // namespace sa

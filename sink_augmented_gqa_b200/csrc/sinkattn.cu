@@ -185,14 +185,15 @@ bool make_matrix_map(CUtensorMap* map, const void* base, long long cols, long lo
 // Tensor map over a strided [B][T][H][d] bf16 activation (inner dim
 // contiguous, other strides in elements, multiples of 8): dims {d, T, H, B},
 // box {CB, 128, 1, 1} -- one 128-row query tile of one head per CB-wide
-// column block; rows past T read as zeros.
+// column block (or box_rows rows of each of box_heads heads, one after
+// another); rows past T read as zeros.
 bool make_rows_map(CUtensorMap* map, const void* base, int d, int T, int H, int B,
-                   const int64_t st[3], int cb, int box_rows = 128) {
+                   const int64_t st[3], int cb, int box_rows = 128, int box_heads = 1) {
   EncodeTiledFn enc = encode_fn();
   if (enc == nullptr || T < 1) return false;
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
   const cuuint64_t strides[3] = {(cuuint64_t)st[1] * 2, (cuuint64_t)st[2] * 2, (cuuint64_t)st[0] * 2};
-  const cuuint32_t box[4] = {(cuuint32_t)cb, (cuuint32_t)box_rows, 1, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)cb, (cuuint32_t)box_rows, (cuuint32_t)box_heads, 1};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims,
                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -397,9 +398,68 @@ sa_status with_sched_slot(cudaStream_t s, F&& launch) {
   return SA_OK;
 }
 
+// Keys per tile of prefill_kernel<d>.
+int prefill_tile_keys(int d) {
+  return d == 64 ? PrefillCfg<64>::BN : d == 96 ? PrefillCfg<96>::BN : PrefillCfg<128>::BN;
+}
+
+// How a prefill on a quantised cache cuts its work into items. pack: a tile's
+// 128 rows are tpos positions of that many query heads (1, or the KV group's);
+// splits: parts of each item's key tiles, where the items leave SMs without
+// work. Of all choices the one whose slowest SM is through first, in key tiles
+// of one query tile (1.1 us; 1.5 us where both query tiles of an item have
+// rows), two of them an item's start and end, parts adding a launch (~4 us)
+// and their partials' traffic. A whole call with and without this choice, d =
+// 64, behind 16,384 rows: 16 rows of 64 / 8 heads (8 heads a tile, 17 parts)
+// 31 us against 158; 128 rows (4 parts) 75 against 159; 900 rows of 4 / 4 heads
+// (9 parts) 44 against 206. Behind 600 rows, 60 rows of 16 / 2 heads: one head a
+// tile, no parts, 15.2; packed 19.1.
+struct PrefillSplit {
+  int pack, tpos, splits;
+  long long items;   // parts counted
+};
+constexpr int kSplitTiles = 2;     // key tiles of a part, at least
+constexpr int kSplitSlots = 160;   // items of a split launch, at most
+
+PrefillSplit plan_prefill(const sa_kv_cache* c, const sa_attn_args* a) {
+  PrefillSplit best = {1, 128, 1, 0};
+  float least = INFINITY;
+  const int qm = a->n_q / c->n_kv, bn = prefill_tile_keys(c->d);
+  const long long slots = num_sms() < kSplitSlots ? num_sms() : kSplitSlots;
+  const float part_us = (float)a->B * a->T * a->n_q * (c->d + 2) * 8.f / 3e6f;   // at 3 TB/s
+  for (int pack = 1; pack <= qm && pack <= 16; pack += qm > 1 ? qm - 1 : 1) {
+    const int tpos = 128 / pack;
+    const long long items = ((long long)a->T + 2 * tpos - 1) / (2 * tpos) * (a->n_q / pack) * a->B;
+    const long long all = a->offset + a->T, band = (long long)a->window - 1 + 2 * tpos;
+    const long long tiles = ((a->window > 0 && band < all ? band : all) + bn - 1) / bn;
+    for (long long S = 1; S == 1 || (S <= slots / items && S <= tiles / kSplitTiles); ++S) {
+      const float cost = (float)((items * S + slots - 1) / slots) * ((float)((tiles + S - 1) / S) + 2.f) *
+                             (a->T > tpos ? 1.5f : 1.1f) +
+                         (S > 1 ? 4.f + part_us * S : 0.f);
+      if (cost < least) {
+        least = cost;
+        best = {pack, tpos, (int)S, items * S};
+      }
+    }
+  }
+  return best;
+}
+
+// Workspace bytes of the parts of a prefill of T rows at c's offset whatever
+// its n_q; 0 where the key tiles are too few for two parts.
+size_t split_ws_bytes(const sa_kv_cache* c, int T, int window) {
+  const long long all = c->offset + T, band = (long long)window - 1 + 256;
+  const long long keys = window > 0 && band < all ? band : all;
+  if ((keys + prefill_tile_keys(c->d) - 1) / prefill_tile_keys(c->d) < 2 * kSplitTiles) return 0;
+  return (size_t)kSplitSlots * 256 * (c->d + 2) * 4;
+}
+
+// parts: with FINE, split_ws_bytes() of workspace.
 template <int D, bool FINE>
-sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, cudaStream_t stream) {
+sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, void* parts, cudaStream_t stream) {
   using Cfg = PrefillCfg<D>;
+  PrefillSplit pl = {1, 128, 1, 0};
+  if (FINE) pl = plan_prefill(c, a);
   CUtensorMap tmQ, tmK, tmV;
   // a ring exposes all of its rows (positions outside the band are masked)
   const long long rows = c->ring > 0 ? (long long)c->cap : a->offset + a->T;
@@ -408,9 +468,10 @@ sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, 
   // its output rows only after it has read it.
   const void* qsrc = a->rope_fused ? a->out : a->q;
   const int64_t* qst = a->rope_fused ? a->out_strides : a->q_strides;
-  if (!make_rows_map(&tmQ, qsrc, D, a->T, a->n_q, a->B, qst, Cfg::CB)) return SA_ERR_CUDA;
+  if (!make_rows_map(&tmQ, qsrc, D, a->T, a->n_q, a->B, qst, Cfg::CB, pl.tpos, pl.pack)) return SA_ERR_CUDA;
   CUtensorMap tmO;   // the output tiles are stored through the same box shape
-  if (!make_rows_map(&tmO, a->out, D, a->T, a->n_q, a->B, a->out_strides, Cfg::CB)) return SA_ERR_CUDA;
+  if (!make_rows_map(&tmO, a->out, D, a->T, a->n_q, a->B, a->out_strides, Cfg::CB, pl.tpos, pl.pack))
+    return SA_ERR_CUDA;
   // The box is one BN-row K/V tile: the kernel's expect-tx byte count and
   // ring-slot size are both Cfg::KV_BYTES = BN * D * 2.
   static_assert(Cfg::KV_BYTES == (uint32_t)Cfg::BN * D * 2, "tile size");
@@ -439,15 +500,22 @@ sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, 
   p.window = a->window > 0 ? a->window : 0;
   p.scale_log2 = a->sm_scale * 1.4426950408889634f;
   p.rope = a->rope_fused ? 1 : 0;
-  p.n_pairs = (a->T + 255) / 256;
+  p.n_pairs = (a->T + 2 * pl.tpos - 1) / (2 * pl.tpos);
   p.ring_cap = c->ring > 0 ? c->cap : 0;
-  static std::atomic<uint64_t> smem_set{0};
+  p.pack = pl.pack;
+  p.tpos = pl.tpos;
+  p.splits = pl.splits;
+  p.part_ml = static_cast<float2*>(parts);
+  p.part_o = pl.splits > 1 ? static_cast<float*>(parts) + 2 * 256 * (size_t)kSplitSlots : nullptr;
+  const bool in_parts = FINE && (pl.pack > 1 || pl.splits > 1);
+  const auto kernel = in_parts ? sa::prefill_kernel<D, true, true> : sa::prefill_kernel<D, FINE>;
+  static std::atomic<uint64_t> smem_set[2] = {};
   {
-    const sa_status sm = set_smem_once(sa::prefill_kernel<D, FINE>, Cfg::SMEM_BYTES, smem_set);
+    const sa_status sm = set_smem_once(kernel, Cfg::SMEM_BYTES, smem_set[in_parts]);
     if (sm != SA_OK) return sm;
   }
   // persistent: one CTA per SM (or per item when there are fewer)
-  const long long n_items = (long long)p.n_pairs * a->n_q * a->B;
+  const long long n_items = FINE ? pl.items : (long long)p.n_pairs * a->n_q * a->B;
   const int grid = (int)(n_items < num_sms() ? n_items : num_sms());
   p.sched_slot = slot;
   // Programmatic stream serialization: the kernel's set-up overlaps the tail
@@ -463,8 +531,15 @@ sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, 
   lc.stream = stream;
   lc.attrs = attr;
   lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, sa::prefill_kernel<D, FINE>, tmQ, tmK, tmV, tmO, p);
-  return (last_launch_status() == SA_OK && e == cudaSuccess) ? SA_OK : SA_ERR_CUDA;
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, tmQ, tmK, tmV, tmO, p);
+  if (last_launch_status() != SA_OK || e != cudaSuccess) return SA_ERR_CUDA;
+  if (pl.splits > 1) {
+    constexpr int kRows = 256 / (D / 4);
+    const long long blocks = ((long long)a->B * a->T * a->n_q + kRows - 1) / kRows;
+    sa::prefill_merge_kernel<D><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    return last_launch_status();
+  }
+  return SA_OK;
 }
 
 // Band layers whose key window fits the packed-head kernel: d = 64, a
@@ -895,9 +970,9 @@ sa_status launch_stage(sa_kv_cache* c, const sa_attn_args* a, bool stage_q, cuda
 
 // Prefill of the rows in a (T > 0) over bf16 cache c: stage(stage_q) puts the
 // call's K/V rows into c and, with stage_q, the rotated queries into a->out;
-// then the attention kernel (FINE: its lse to fp32).
+// then the attention kernel (FINE: of a quantised cache, with workspace for its parts).
 template <bool FINE, typename F>
-sa_status run_prefill(const sa_kv_cache* c, const sa_attn_args* a, cudaStream_t s, F&& stage) {
+sa_status run_prefill(const sa_kv_cache* c, const sa_attn_args* a, void* parts, cudaStream_t s, F&& stage) {
   const cudaEvent_t ev0 = g_prefill_ev_before, ev1 = g_prefill_ev_after;
   const int band_n = band_columns(c, a);
   if (band_n > 0) {
@@ -917,9 +992,9 @@ sa_status run_prefill(const sa_kv_cache* c, const sa_attn_args* a, cudaStream_t 
     if (r != SA_OK) return r;
     if (ev0 != nullptr && cudaEventRecord(ev0, s) != cudaSuccess) return SA_ERR_CUDA;
     switch (c->d) {
-      case 64: r = launch_prefill<64, FINE>(c, a, slot, s); break;
-      case 96: r = launch_prefill<96, FINE>(c, a, slot, s); break;
-      default: r = launch_prefill<128, FINE>(c, a, slot, s); break;
+      case 64: r = launch_prefill<64, FINE>(c, a, slot, parts, s); break;
+      case 96: r = launch_prefill<96, FINE>(c, a, slot, parts, s); break;
+      default: r = launch_prefill<128, FINE>(c, a, slot, parts, s); break;
     }
     if (ev1 != nullptr && cudaEventRecord(ev1, s) != cudaSuccess) return SA_ERR_CUDA;
     return r;
@@ -932,9 +1007,12 @@ long long quant_prefix(const sa_kv_cache* c, int window) {
 }
 
 // Workspace of sa_attn_prefill_quant: bf16 K and V rows of those positions
-// and of the call's T.
-size_t quant_ws_bytes(const sa_kv_cache* c, int T, int window) {
+// and of the call's T, then the attention's parts.
+size_t quant_row_bytes(const sa_kv_cache* c, int T, int window) {
   return 2 * (size_t)c->B * c->n_kv * (size_t)(quant_prefix(c, window) + T) * c->d * 2;
+}
+size_t quant_ws_bytes(const sa_kv_cache* c, int T, int window) {
+  return quant_row_bytes(c, T, window) + split_ws_bytes(c, T, window);
 }
 
 // The launch before the attention of sa_attn_prefill_quant: the call's rows into
@@ -1309,7 +1387,7 @@ sa_status sa_attn_prefill(sa_kv_cache* cache, const sa_attn_args* a, sa_stream_t
   bool staged = false;
   // one launch: the call's K rows rotated (when RoPE is fused) and appended
   // with V, and (stage_q) the rotated queries staged in `out`
-  st = run_prefill<false>(cache, a, s, [&](bool stage_q) -> sa_status {
+  st = run_prefill<false>(cache, a, nullptr, s, [&](bool stage_q) -> sa_status {
     const sa_status r = launch_stage(cache, a, stage_q, s);
     staged = r == SA_OK;
     return r;
@@ -1341,7 +1419,8 @@ sa_status sa_attn_prefill_quant(sa_kv_cache* cache, const sa_attn_args* a, void*
   if (rows > INT32_MAX) return SA_ERR_CAPACITY;
   sa_kv_cache w;
   char* base = static_cast<char*>(workspace);
-  st = sa_kv_cache_init(&w, base, base + quant_ws_bytes(cache, a->T, a->window) / 2, cache->B, (int32_t)rows,
+  const size_t row_bytes = quant_row_bytes(cache, a->T, a->window);
+  st = sa_kv_cache_init(&w, base, base + row_bytes / 2, cache->B, (int32_t)rows,
                         cache->n_kv, cache->d);
   if (st != SA_OK) return st;
   w.offset = prefix;
@@ -1353,7 +1432,7 @@ sa_status sa_attn_prefill_quant(sa_kv_cache* cache, const sa_attn_args* a, void*
     wa.max_pos = (int32_t)(a->max_pos - lo);
   }
   bool appended = false;
-  st = run_prefill<true>(&w, &wa, s, [&](bool stage_q) -> sa_status {
+  st = run_prefill<true>(&w, &wa, base + row_bytes, s, [&](bool stage_q) -> sa_status {
     const sa_status r = launch_quant_stage(cache, &w, a, lo, stage_q, s);
     appended = r == SA_OK;
     return r;

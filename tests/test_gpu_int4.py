@@ -558,6 +558,29 @@ def test_prefill_quant_matches_oracle(cuda_device, fmt, over, window, off, T):
         assert np.array_equal(to64(gk), _stands_for(fmt, k_rot)) and np.array_equal(to64(gv), _stands_for(fmt, to64(v)))
 
 
+@pytest.mark.parametrize("over", [dict(B=1, n_q=8, n_kv=1, d=64), dict(B=2, n_q=6, n_kv=2, d=96),
+                                  dict(B=1, n_q=14, n_kv=2, d=128), dict(B=1, n_q=16, n_kv=1, d=64),
+                                  dict(B=2, n_q=20, n_kv=1, d=64), dict(B=3, n_q=5, n_kv=1, d=128)],
+                         ids=["8x", "3x", "7x", "16x", "20x", "5x"])
+@pytest.mark.parametrize("off,T,window", [(4000, 1, 0), (4000, 2, 0), (1500, 17, 0), (5003, 77, 0), (900, 300, 0),
+                                          (4000, 40, 1500), (3000, 513, 700), (0, 1025, 0)])
+def test_prefill_quant_of_few_rows_behind_many(cuda_device, over, off, T, window):
+    # heads of a KV group side by side in a tile, key tiles cut into parts: rows
+    # whose part holds no key, parts without tiles, ends inside a tile
+    cfg, cache, oracle, cos, sin = _setup(over, "int4", off, T)
+    sinks = wl.sinks(cfg) if T % 2 else None
+    q, k, v = wl.qkv(cfg, T, step=1)
+    nb = sa.prefill_quant_workspace(cache, T, window).numel()
+    ws = torch.full((nb + 256,), 0xFF, dtype=torch.uint8, device=DEV)   # NaNs, whatever is read unwritten
+    out, lse = sa.attn_prefill_quant(cache, q.to(DEV), k.to(DEV), v.to(DEV), None if sinks is None else sinks.to(DEV),
+                                     window, cfg.sm_scale, cos, sin, workspace=ws, return_lse=True)
+    torch.cuda.synchronize()
+    ref, ref_lse, _ = oracle.call(q, k, v, sinks, window)
+    check_bf16_output(out, ref, "prefill in parts")
+    check_lse(lse, ref_lse, "prefill in parts")
+    assert (ws[nb:] == 0xFF).all()
+
+
 @pytest.mark.parametrize("fmt", ["int4", "fp8"])
 def test_prefill_quant_on_a_ring(cuda_device, fmt):
     cfg, cache, oracle, cos, sin = _setup(dict(B=2, n_q=8, n_kv=2, d=64), fmt, 1000, 700, ring_window=128)
