@@ -582,6 +582,53 @@ def test_prefill_quant_of_few_rows_behind_many(cuda_device, over, off, T, window
 
 
 @pytest.mark.parametrize("fmt", ["int4", "fp8"])
+def test_prefill_quant_in_parts_in_graphs_and_streams(cuda_device, fmt):
+    # two layers' calls captured over one workspace and replayed in turn, `out`
+    # being `q` in the second; then both at a time on streams of their own
+    over, off, T = dict(B=1, n_q=16, n_kv=2, d=64), 4000, 20
+    stream, made, ws = torch.cuda.Stream(), [], None
+    for i, window in enumerate((0, 1000)):
+        cfg, cache, oracle, cos, sin = _setup(over, fmt, off, T, seed=i)
+        q, k, v = wl.qkv(cfg, T, step=1)
+        ref, ref_lse, _ = oracle.call(q, k, v, None, window)
+        q, k, v = (t.to(DEV) for t in (q, k, v))
+        q0, out, lse = q.clone(), q if i else torch.empty_like(q), torch.empty(1, 16, T, device=DEV)
+        if ws is None:
+            ws = sa.prefill_quant_workspace(cache, T)
+        snap = cache.snapshot()
+
+        def call(w, cache=cache, snap=snap, q=q, k=k, v=v, window=window, cos=cos, sin=sin, out=out, lse=lse):
+            cache.restore(snap)
+            sa.attn_prefill_quant(cache, q, k, v, None, window, cfg.sm_scale, cos, sin, workspace=w, out=out,
+                                  return_lse=True, lse=lse)
+
+        stream.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            call(ws)
+        made.append((graph, call, q, q0, out, lse, ref, ref_lse, cache))
+
+    def check(what):
+        torch.cuda.synchronize()
+        for _, _, _, _, out, lse, ref, ref_lse, _ in made:
+            check_bf16_output(out, ref, what)
+            check_lse(lse, ref_lse, what)
+
+    for _ in range(2):
+        for graph, _, q, q0, *_ in made:
+            q.copy_(q0)
+            graph.replay()
+        check("replayed in turn")
+    for _, call, q, q0, *_ in made:
+        q.copy_(q0)
+    torch.cuda.synchronize()
+    for (_, call, *_), st in zip(made, (torch.cuda.Stream(), torch.cuda.Stream())):
+        with torch.cuda.stream(st):
+            call(torch.empty_like(ws))
+    check("two streams")
+
+
+@pytest.mark.parametrize("fmt", ["int4", "fp8"])
 def test_prefill_quant_on_a_ring(cuda_device, fmt):
     cfg, cache, oracle, cos, sin = _setup(dict(B=2, n_q=8, n_kv=2, d=64), fmt, 1000, 700, ring_window=128)
     sinks = wl.sinks(cfg)
