@@ -195,6 +195,11 @@ def _empty4(B, T, H, d, device):
     return torch.empty_strided((B, T, H, d), (T * H * d, H * d, d, 1), dtype=torch.bfloat16, device=device)
 
 
+def _empty_out(q):
+    """A dense bf16 tensor of q's shape (empty_like where that is dense: cheaper still)."""
+    return torch.empty_like(q) if q.is_contiguous() else _empty4(*q.shape, q.device)
+
+
 def _empty_lse(B, n_q, T, device):
     return torch.empty_strided((B, n_q, T), (n_q * T, T, 1), dtype=torch.float32, device=device)
 
@@ -330,19 +335,21 @@ class KVCache:
         B, T, H, d = raw.B, stop - start, raw.n_kv, raw.d
         if T < 0:
             raise ValueError("stop is below start")
-        ks = vs = (T * H * d, H * d, d)
-        if k_out is None:
-            k_out = _empty4(B, T, H, d, self.k.device)
-        else:
+        ks = vs = None
+        if k_out is not None:
             ks = _view4("k_out", k_out)
-        if v_out is None:
-            v_out = _empty4(B, T, H, d, self.k.device)
-        else:
+        if v_out is not None:
             vs = _view4("v_out", v_out)
-        if k_out.shape != (B, T, H, d) or v_out.shape != (B, T, H, d):
+        if (ks and k_out.shape != (B, T, H, d)) or (vs and v_out.shape != (B, T, H, d)):
             raise ValueError(f"k_out and v_out must be {(B, T, H, d)}")
-        _check(lib().sa_kv_read(ctypes.byref(raw), start, T, k_out.data_ptr(), _I64x3(ks[0], ks[1], ks[2]),
-                                v_out.data_ptr(), _I64x3(vs[0], vs[1], vs[2]), _raw_stream(self.k)), "sa_kv_read")
+        dense = _I64x3(T * H * d, H * d, d)
+        if ks is None:
+            k_out = _empty4(B, T, H, d, self.k.device)
+        if vs is None:
+            v_out = torch.empty_like(k_out) if ks is None else _empty4(B, T, H, d, self.k.device)
+        _check(lib().sa_kv_read(ctypes.byref(raw), start, T, k_out.data_ptr(), _I64x3(*ks[:3]) if ks else dense,
+                                v_out.data_ptr(), _I64x3(*vs[:3]) if vs else dense, _raw_stream(self.k)),
+               "sa_kv_read")
         return k_out, v_out
 
     def snapshot(self):
@@ -392,7 +399,7 @@ def attn_prefill(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=None, ro
     [0, offset + T). Returns out [B,T,n_q,d] bf16 (and lse [B,n_q,T] fp32)."""
     B, T, n_q, d = q.shape
     if out is None:
-        out = _empty4(B, T, n_q, d, q.device)
+        out = _empty_out(q)
     if return_lse and lse is None:
         lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
@@ -416,7 +423,7 @@ def attn_prefill_quant(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=No
     elif not (workspace.is_cuda and workspace.is_contiguous()):
         raise TypeError("workspace must be a contiguous CUDA tensor")
     if out is None:
-        out = _empty4(B, T, n_q, d, q.device)
+        out = _empty_out(q)
     if return_lse and lse is None:
         lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
@@ -442,7 +449,7 @@ def attn_decode(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=None, rop
     if workspace is None:
         workspace = decode_workspace(B, n_q, cache.raw.n_kv, d, q.device)
     if out is None:
-        out = _empty4(B, T, n_q, d, q.device)
+        out = _empty_out(q)
     if return_lse and lse is None:
         lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
@@ -533,7 +540,7 @@ def attn_decode_static(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=No
     shared by every call -- do not overlap calls on the GPU."""
     B, T, n_q, d = q.shape
     if out is None:
-        out = _empty4(B, T, n_q, d, q.device)
+        out = _empty_out(q)
     if return_lse and lse is None:
         lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
