@@ -412,6 +412,8 @@ def test_zero_wait_limit_is_right_or_reported(cuda_device, over, off):
     cache.restore(snap)
     for step in range(2):
         _decode(cfg, cache, oracle, cos, sin, 0, None, step + 1, ws, "after timeout")
+    out = sa.attn_prefill_quant(cache, q2, k2, v2, None, 0, cfg.sm_scale, cos, sin)
+    check_bf16_output(out, oracle.call(q2, k2, v2, None, 0)[0], "prefill after timeout")
     assert sa.device_status() == "SA_OK"
 
 
