@@ -353,7 +353,7 @@ sa_status sa_attn_prefill_quant(sa_kv_cache* cache, const sa_attn_args* args, vo
 /* Workspace bytes of sa_attn_prefill_quant for T rows at the cache's present
  * offset: K and V of T + (window > 0 ? min(offset, window - 1) : offset)
  * positions in bf16, and where those are long enough to be shared out (four
- * key tiles, of 128, 96 or 64 keys for d = 64, 96, 128) 160 * 256 fp32 rows of
+ * key tiles, of 128, 96 or 64 keys for d = 64, 96, 128) 320 * 256 fp32 rows of
  * d + 2. 0 for an invalid cache or T < 1. */
 size_t sa_attn_prefill_quant_workspace_size(const sa_kv_cache* cache, int32_t T, int32_t window);
 

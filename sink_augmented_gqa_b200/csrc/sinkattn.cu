@@ -419,21 +419,24 @@ struct PrefillSplit {
   long long items;   // parts counted
 };
 constexpr int kSplitTiles = 2;     // key tiles of a part, at least
-constexpr int kSplitSlots = 160;   // items of a split launch, at most
+// Items of a split launch, at most: two waves, so that items which half fill a
+// second one can be cut finer (300 rows of 64 / 8 heads behind 16,384: 80 items of
+// 8 heads in 3 parts, 172 us, against 214 of 128 whole ones).
+constexpr int kSplitSlots = 320;
 
 PrefillSplit plan_prefill(const sa_kv_cache* c, const sa_attn_args* a) {
   PrefillSplit best = {1, 128, 1, 0};
   float least = INFINITY;
   const int qm = a->n_q / c->n_kv, bn = prefill_tile_keys(c->d);
-  const long long slots = num_sms() < kSplitSlots ? num_sms() : kSplitSlots;
+  const long long sms = num_sms();
   const float part_us = (float)a->B * a->T * a->n_q * (c->d + 2) * 8.f / 3e6f;   // at 3 TB/s
   for (int pack = 1; pack <= qm && pack <= 16; pack += qm > 1 ? qm - 1 : 1) {
     const int tpos = 128 / pack;
     const long long items = ((long long)a->T + 2 * tpos - 1) / (2 * tpos) * (a->n_q / pack) * a->B;
     const long long all = a->offset + a->T, band = (long long)a->window - 1 + 2 * tpos;
     const long long tiles = ((a->window > 0 && band < all ? band : all) + bn - 1) / bn;
-    for (long long S = 1; S == 1 || (S <= slots / items && S <= tiles / kSplitTiles); ++S) {
-      const float cost = (float)((items * S + slots - 1) / slots) * ((float)((tiles + S - 1) / S) + 2.f) *
+    for (long long S = 1; S == 1 || (S <= kSplitSlots / items && S <= tiles / kSplitTiles); ++S) {
+      const float cost = (float)((items * S + sms - 1) / sms) * ((float)((tiles + S - 1) / S) + 2.f) *
                              (a->T > tpos ? 1.5f : 1.1f) +
                          (S > 1 ? 4.f + part_us * S : 0.f);
       if (cost < least) {

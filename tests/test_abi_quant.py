@@ -124,7 +124,7 @@ def test_prefill_quant_workspace_size(L):
     row = 2 * 3 * 2 * 96 * 2
     assert size(5) == 5 * row
     c.offset = c.high_water = 1000
-    parts = 160 * 256 * (96 + 2) * 4       # 4 key tiles of 96 and more may be cut into parts
+    parts = 320 * 256 * (96 + 2) * 4       # 4 key tiles of 96 and more may be cut into parts
     assert size(5) == 1005 * row + parts and size(5, 128) == 132 * row + parts and size(5, 1) == 5 * row
     assert size(5, 5000) == 1005 * row + parts
     assert size(5, 33) == 37 * row and size(5, 34) == 38 * row + parts    # 288 and 289 keys
