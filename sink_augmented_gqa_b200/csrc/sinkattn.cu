@@ -435,7 +435,7 @@ PrefillSplit plan_prefill(const sa_kv_cache* c, const sa_attn_args* a) {
     const long long items = ((long long)a->T + 2 * tpos - 1) / (2 * tpos) * (a->n_q / pack) * a->B;
     const long long all = a->offset + a->T, band = (long long)a->window - 1 + 2 * tpos;
     const long long tiles = ((a->window > 0 && band < all ? band : all) + bn - 1) / bn;
-    for (long long S = 1; S == 1 || (S <= kSplitSlots / items && S <= tiles / kSplitTiles); ++S) {
+    for (long long S = 1; S == 1 || (S <= kSplitSlots / items && S <= tiles / kSplitTiles); S += S < 16 ? 1 : S / 8) {
       const float cost = (float)((items * S + sms - 1) / sms) * ((float)((tiles + S - 1) / S) + 2.f) *
                              (a->T > tpos ? 1.5f : 1.1f) +
                          (S > 1 ? 4.f + part_us * S : 0.f);
