@@ -819,36 +819,66 @@ __global__ void __launch_bounds__(384, 1)
   }
 }
 
-// Joins the parts of prefill_kernel<D, true, true>: a row's D / 4 lanes sum its
-// partials relative to their largest max (the sink is in part 0) and write the
-// row and its lse. Its reads, 4 (d + 2) bytes a row and part, come from L2.
-template <int D>
-__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p) {
-  constexpr int LANES = D / 4, RB = 256 / LANES;
-  const int rb = threadIdx.x / LANES, ch = threadIdx.x - rb * LANES;
-  const long long n = (long long)p.B * p.T * p.n_q, at = (long long)blockIdx.x * RB + rb;
-  if (rb >= RB || at >= n) return;
-  const int h = (int)(at % p.n_q), b = (int)(at / p.n_q / p.T), i = (int)(at / p.n_q % p.T);
-  const int hi = h / p.pack, m_i = h - hi * p.pack, pair = i / (2 * p.tpos), rest = i - pair * 2 * p.tpos;
-  const int rt = rest / p.tpos, t = rest - rt * p.tpos;
-  const int heads = p.n_q / p.pack;
-  const long long item = ((long long)(p.n_pairs - 1 - pair) * heads * p.B + (long long)b * heads + hi) * p.splits;
-  const long long row = item * 256 + 128 * rt + m_i * p.tpos + t;   // of part 0; the next ones 256 rows on
-  float M = -INFINITY;
-  for (int k = 0; k < p.splits; ++k) M = fmaxf(M, p.part_ml[row + 256LL * k].x);
-  float L = 0.f;
+// Joins the parts of prefill_kernel<D, true, true>: `groups` times D / 4 lanes
+// sum a row's partials, each group every groups-th, relative to their largest
+// max (the sink is in part 0), and the first joins the groups' sums and writes
+// the row and its lse. Its reads, 4 (d + 2) bytes a row and part, come from L2,
+// and a lane waits for few of them at a time: with one group for all 43 parts of
+// 16 rows of 8 / 1 heads behind 16,384 a whole call took 24.8 us instead of 16.8.
+// GROUPS: more than one.
+template <int D, bool GROUPS>
+__global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p, const int n_groups) {
+  constexpr int LANES = D / 4;
+  const int groups = GROUPS ? n_groups : 1;
+  __shared__ float4 sum_o[GROUPS ? 256 : 1];
+  __shared__ float2 sum_ml[GROUPS ? 256 : 1];
+  const int rows = 256 / (LANES * groups), rb = threadIdx.x / (LANES * groups);
+  const int in_row = threadIdx.x - rb * LANES * groups, grp = in_row / LANES, ch = in_row - grp * LANES;
+  const long long n = (long long)p.B * p.T * p.n_q, at = (long long)blockIdx.x * rows + rb;
+  const bool live = rb < rows && at < n;
+  if (!GROUPS && !live) return;
+  const int h = live ? (int)(at % p.n_q) : 0, b = live ? (int)(at / p.n_q / p.T) : 0;
+  const int i = live ? (int)(at / p.n_q % p.T) : 0;
+  float M = -INFINITY, L = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < p.splits; ++k) {
-    const float2 ml = p.part_ml[row + 256LL * k];
-    const float w = ex2(ml.x - M);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + (row + 256LL * k) * D + 4 * ch);
-    L = fmaf(w, ml.y, L);
+  auto add = [&](float w, float l, const float4& v) {
+    L = fmaf(w, l, L);
     o.x = fmaf(w, v.x, o.x);
     o.y = fmaf(w, v.y, o.y);
     o.z = fmaf(w, v.z, o.z);
     o.w = fmaf(w, v.w, o.w);
+  };
+  // weight of a partial relative to 2^M (0 for one without keys, also in a group of such)
+  auto weight = [&](float m) { return ex2(m - (GROUPS && M == -INFINITY ? 0.f : M)); };
+  if (live) {
+    const int hi = h / p.pack, m_i = h - hi * p.pack, pair = i / (2 * p.tpos), rest = i - pair * 2 * p.tpos;
+    const int rt = rest / p.tpos, t = rest - rt * p.tpos;
+    const int heads = p.n_q / p.pack;
+    const long long item = ((long long)(p.n_pairs - 1 - pair) * heads * p.B + (long long)b * heads + hi) * p.splits;
+    const long long row = item * 256 + 128 * rt + m_i * p.tpos + t;   // of part 0; the next ones 256 rows on
+#pragma unroll 4
+    for (int k = grp; k < p.splits; k += groups) M = fmaxf(M, p.part_ml[row + 256LL * k].x);
+#pragma unroll 4
+    for (int k = grp; k < p.splits; k += groups) {
+      const float2 ml = p.part_ml[row + 256LL * k];
+      add(weight(ml.x), ml.y, *reinterpret_cast<const float4*>(p.part_o + (row + 256LL * k) * D + 4 * ch));
+    }
   }
+  if constexpr (GROUPS) {
+    sum_o[threadIdx.x] = o;
+    sum_ml[threadIdx.x] = make_float2(M, L);
+    __syncthreads();
+    if (live && grp == 0) {
+      for (int k = 1; k < groups; ++k) M = fmaxf(M, sum_ml[threadIdx.x + k * LANES].x);
+      L = 0.f;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < groups; ++k) {
+        const float2 ml = sum_ml[threadIdx.x + k * LANES];
+        add(weight(ml.x), ml.y, sum_o[threadIdx.x + k * LANES]);
+      }
+    }
+  }
+  if (!live || grp != 0) return;
   const float inv = 1.0f / L;
   *reinterpret_cast<uint2*>(p.out + b * p.os0 + i * p.os1 + h * p.os2 + 4 * ch) =
       make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));

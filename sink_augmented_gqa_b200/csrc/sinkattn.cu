@@ -411,8 +411,8 @@ int prefill_tile_keys(int d) {
 // rows), two of them an item's start and end, parts adding a launch (~4 us)
 // and their partials' traffic. A whole call with and without this choice, d =
 // 64, behind 16,384 rows: 16 rows of 64 / 8 heads (8 heads a tile, 17 parts)
-// 31 us against 158; 128 rows (4 parts) 75 against 159; 900 rows of 4 / 4 heads
-// (9 parts) 44 against 206. Behind 600 rows, 60 rows of 16 / 2 heads: one head a
+// 29 us against 158; 128 rows (4 parts) 75 against 159; 900 rows of 4 / 4 heads
+// (9 parts) 45 against 206. Behind 600 rows, 60 rows of 16 / 2 heads: one head a
 // tile, no parts, 15.2; packed 19.1.
 struct PrefillSplit {
   int pack, tpos, splits;
@@ -537,9 +537,15 @@ sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, 
   const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, tmQ, tmK, tmV, tmO, p);
   if (last_launch_status() != SA_OK || e != cudaSuccess) return SA_ERR_CUDA;
   if (pl.splits > 1) {
-    constexpr int kRows = 256 / (D / 4);
-    const long long blocks = ((long long)a->B * a->T * a->n_q + kRows - 1) / kRows;
-    sa::prefill_merge_kernel<D><<<(unsigned)blocks, 256, 0, stream>>>(p);
+    // four parts or more for each group of lanes
+    int groups = 1;
+    while (groups * 2 * (D / 4) <= 256 && pl.splits >= groups * 8) groups *= 2;
+    const long long rows = 256 / (D / 4 * groups);
+    const long long blocks = ((long long)a->B * a->T * a->n_q + rows - 1) / rows;
+    if (groups > 1)
+      sa::prefill_merge_kernel<D, true><<<(unsigned)blocks, 256, 0, stream>>>(p, groups);
+    else
+      sa::prefill_merge_kernel<D, false><<<(unsigned)blocks, 256, 0, stream>>>(p, 1);
     return last_launch_status();
   }
   return SA_OK;
