@@ -133,6 +133,8 @@ struct RowsCfg {
 template <int D, int NR>
 __global__ void __launch_bounds__(256) kv_append_i4_kernel(const RowsParams p) {
   using C = RowsCfg<D>;
+  griddep_launch_dependents();
+  griddep_wait();
   const int g = blockIdx.y, b = blockIdx.z;
   const int rb = threadIdx.x / C::CH, ch = threadIdx.x - rb * C::CH;
   const int t0 = blockIdx.x * (C::RB * NR) + rb;
@@ -228,6 +230,8 @@ __device__ __forceinline__ uint4 row8_bf16(const StoredRow8<KIND>& x) {
 template <int D, int KIND, int NR>
 __global__ void __launch_bounds__(256) kv_read_kernel(const RowsParams p) {
   using C = RowsCfg<D>;
+  griddep_launch_dependents();
+  griddep_wait();
   const int g = blockIdx.y, b = blockIdx.z;
   const int rb = threadIdx.x / C::CH, ch = threadIdx.x - rb * C::CH;
   if (rb >= C::RB) return;

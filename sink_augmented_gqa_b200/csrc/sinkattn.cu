@@ -867,6 +867,23 @@ sa::RowsParams rows_params(const sa_kv_cache* c, const void* k, const int64_t ks
   return p;
 }
 
+// Launches a row kernel, which waits for the kernel ahead of it on the stream
+// (programmatic stream serialization: its launch overlaps that one's drain, as a
+// decode's does).
+sa_status launch_rows(void (*kernel)(sa::RowsParams), dim3 grid, const sa::RowsParams& p, cudaStream_t stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(256);
+  lc.stream = stream;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p);
+  return (last_launch_status() == SA_OK && e == cudaSuccess) ? SA_OK : SA_ERR_CUDA;
+}
+
 // Grid of a row kernel: blocks of rows x KV heads x sequences, with 4 rows a
 // thread where that still gives every SM four blocks (*four), else 1.
 template <int D>
@@ -887,11 +904,7 @@ sa_status launch_append_i4(const sa_kv_cache* c, const void* k, const int64_t ks
   bool four;
   const sa_status st = rows_grid<D>(c, T, &grid, &four);
   if (st != SA_OK) return st;
-  if (four)
-    sa::kv_append_i4_kernel<D, 4><<<grid, 256, 0, stream>>>(p);
-  else
-    sa::kv_append_i4_kernel<D, 1><<<grid, 256, 0, stream>>>(p);
-  return last_launch_status();
+  return launch_rows(four ? sa::kv_append_i4_kernel<D, 4> : sa::kv_append_i4_kernel<D, 1>, grid, p, stream);
 }
 
 template <int D, int KIND>
@@ -900,11 +913,7 @@ sa_status launch_read(const sa_kv_cache* c, const sa::RowsParams& p, cudaStream_
   bool four;
   const sa_status st = rows_grid<D>(c, p.T, &grid, &four);
   if (st != SA_OK) return st;
-  if (four)
-    sa::kv_read_kernel<D, KIND, 4><<<grid, 256, 0, stream>>>(p);
-  else
-    sa::kv_read_kernel<D, KIND, 1><<<grid, 256, 0, stream>>>(p);
-  return last_launch_status();
+  return launch_rows(four ? sa::kv_read_kernel<D, KIND, 4> : sa::kv_read_kernel<D, KIND, 1>, grid, p, stream);
 }
 
 template <int D>
