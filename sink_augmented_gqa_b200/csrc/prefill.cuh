@@ -830,6 +830,8 @@ template <int D, bool GROUPS>
 __global__ void __launch_bounds__(256) prefill_merge_kernel(const PrefillParams p, const int n_groups) {
   constexpr int LANES = D / 4;
   const int groups = GROUPS ? n_groups : 1;
+  griddep_launch_dependents();
+  griddep_wait();
   __shared__ float4 sum_o[GROUPS ? 256 : 1];
   __shared__ float2 sum_ml[GROUPS ? 256 : 1];
   const int rows = 256 / (LANES * groups), rb = threadIdx.x / (LANES * groups);

@@ -46,6 +46,7 @@ __global__ void __launch_bounds__(256) quant_stage_kernel(const QuantStageParams
   constexpr int HALF = D / 2, PC = D / 16, NR = 4;
   __shared__ __align__(16) __nv_bfloat16 rot[C::RB * D];
   griddep_launch_dependents();
+  griddep_wait();
   const int tid = threadIdx.x;
   const int rb = tid / C::CH, ch = tid - rb * C::CH;
   const long long w_rows = (long long)p.prefix + p.T;

@@ -398,6 +398,24 @@ sa_status with_sched_slot(cudaStream_t s, F&& launch) {
   return SA_OK;
 }
 
+// Launches a kernel of 256 threads a block that waits for the kernel ahead of it
+// on the stream (programmatic stream serialization: its launch overlaps that
+// one's drain, as a decode's does).
+template <typename... P, typename... A>
+sa_status launch_behind(void (*kernel)(P...), dim3 grid, cudaStream_t stream, const A&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(256);
+  lc.stream = stream;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, args...);
+  return (last_launch_status() == SA_OK && e == cudaSuccess) ? SA_OK : SA_ERR_CUDA;
+}
+
 // Keys per tile of prefill_kernel<d>.
 int prefill_tile_keys(int d) {
   return d == 64 ? PrefillCfg<64>::BN : d == 96 ? PrefillCfg<96>::BN : PrefillCfg<128>::BN;
@@ -542,11 +560,8 @@ sa_status launch_prefill(const sa_kv_cache* c, const sa_attn_args* a, int slot, 
     while (groups * 2 * (D / 4) <= 256 && pl.splits >= groups * 8) groups *= 2;
     const long long rows = 256 / (D / 4 * groups);
     const long long blocks = ((long long)a->B * a->T * a->n_q + rows - 1) / rows;
-    if (groups > 1)
-      sa::prefill_merge_kernel<D, true><<<(unsigned)blocks, 256, 0, stream>>>(p, groups);
-    else
-      sa::prefill_merge_kernel<D, false><<<(unsigned)blocks, 256, 0, stream>>>(p, 1);
-    return last_launch_status();
+    return launch_behind(groups > 1 ? sa::prefill_merge_kernel<D, true> : sa::prefill_merge_kernel<D, false>,
+                         dim3((unsigned)blocks), stream, p, groups);
   }
   return SA_OK;
 }
@@ -867,23 +882,6 @@ sa::RowsParams rows_params(const sa_kv_cache* c, const void* k, const int64_t ks
   return p;
 }
 
-// Launches a row kernel, which waits for the kernel ahead of it on the stream
-// (programmatic stream serialization: its launch overlaps that one's drain, as a
-// decode's does).
-sa_status launch_rows(void (*kernel)(sa::RowsParams), dim3 grid, const sa::RowsParams& p, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t lc = {};
-  lc.gridDim = grid;
-  lc.blockDim = dim3(256);
-  lc.stream = stream;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&lc, kernel, p);
-  return (last_launch_status() == SA_OK && e == cudaSuccess) ? SA_OK : SA_ERR_CUDA;
-}
-
 // Grid of a row kernel: blocks of rows x KV heads x sequences, with 4 rows a
 // thread where that still gives every SM four blocks (*four), else 1.
 template <int D>
@@ -904,7 +902,7 @@ sa_status launch_append_i4(const sa_kv_cache* c, const void* k, const int64_t ks
   bool four;
   const sa_status st = rows_grid<D>(c, T, &grid, &four);
   if (st != SA_OK) return st;
-  return launch_rows(four ? sa::kv_append_i4_kernel<D, 4> : sa::kv_append_i4_kernel<D, 1>, grid, p, stream);
+  return launch_behind(four ? sa::kv_append_i4_kernel<D, 4> : sa::kv_append_i4_kernel<D, 1>, grid, stream, p);
 }
 
 template <int D, int KIND>
@@ -913,7 +911,7 @@ sa_status launch_read(const sa_kv_cache* c, const sa::RowsParams& p, cudaStream_
   bool four;
   const sa_status st = rows_grid<D>(c, p.T, &grid, &four);
   if (st != SA_OK) return st;
-  return launch_rows(four ? sa::kv_read_kernel<D, KIND, 4> : sa::kv_read_kernel<D, KIND, 1>, grid, p, stream);
+  return launch_behind(four ? sa::kv_read_kernel<D, KIND, 4> : sa::kv_read_kernel<D, KIND, 1>, grid, stream, p);
 }
 
 template <int D>
@@ -1073,8 +1071,7 @@ sa_status launch_quant_stage(const sa_kv_cache* c, const sa_kv_cache* w, const s
   if (n_new + n_old + n_q > INT32_MAX) return SA_ERR_SHAPE;
   p.n_new = (int)n_new;
   p.n_old = (int)n_old;
-  sa::quant_stage_kernel<D, F8><<<(unsigned)(n_new + n_old + n_q), 256, 0, stream>>>(p);
-  return last_launch_status();
+  return launch_behind(sa::quant_stage_kernel<D, F8>, dim3((unsigned)(n_new + n_old + n_q)), stream, p);
 }
 
 sa_status launch_quant_stage(const sa_kv_cache* c, const sa_kv_cache* w, const sa_attn_args* a, long long lo,
