@@ -5,9 +5,10 @@
 // the ALU pipe (half the issue rate), so the codes go to the tensor cores with
 // as few instructions as possible, and every SM gets the same number of rows.
 //
-// One CTA per SM, 16 consumer warps that take 32 rows each of a 512-row stage
-// (with two CTAs of 8 per SM the scheduler's older one ran ahead and left the
-// other half of the SM's warps for the last fifth of the time). A (sequence,
+// One CTA per SM, 16 consumer warps (d = 128: 12) that take 32 rows each of a
+// 512-row (384-row) stage (with two CTAs of 8 per SM the scheduler's older one
+// ran ahead and left the other half of the SM's warps for the last fifth of the
+// time). A (sequence,
 // KV head) pair's rows count in units of 128. Where the CTAs can be dealt out
 // to the pairs evenly, each pair gets S of them; else the units of all pairs
 // lie in one row and every CTA takes an equal, contiguous share (plan_decode
@@ -38,14 +39,22 @@
 //   the first, x & 0x00F000F0 16 times those of the second, and x >> 8 gives
 //   the other two: 5 instructions for 8 codes (bf16, whose 7 fraction bits
 //   hold one code, takes 7). The offset of 8 goes out at the end, by the sums
-//   of P', which a lane has in fp32.
-// The weights are taken relative to 2^ref with ref = m + E - 6, m a score of the
-//   head that no score so far has exceeded by more than 8 (log2 units) and 2^E
-//   the power of two below the largest |scale_v| that the warp has seen: then
-//   |P'| < 2^15, which f16 holds, with its 11 bits down to 2^-20 of the weight
-//   of m and some to 2^-30. m and E move only when a tile breaks one of the two
-//   bounds, so a tile needs no maximum across lanes, only a vote. Sums, the
-//   merge and the lse go by ref as by a maximum.
+//   of P' in fp32: of P' as rounded to f16, so that a key whose P' is rounded
+//   (to nothing, even) is wrong by that much of its value and no more.
+// p is relative to 2^ref, ref a score of the head that no score so far has
+//   exceeded by more than 8 (log2 units); the sum of p, the merge and the lse
+//   know nothing of V. P' has a power of two of its own for each block of 32
+//   elements and each head, f = 2^(6 - E): blocks and heads do not share one,
+//   since what is large in one may be nothing in another. 2^E is 16 times the
+//   largest p |scale_v| (rounded down to a power of two) found where E last
+//   moved, so a row of negligible weight does not set it, however large; it
+//   moves with ref, up and down, and up where a |scale_v| exceeds 2^(E + 1).
+//   In a tile where none does, P' < 2^(8 + E + 1) f = 2^15, which f16 holds;
+//   in one where E moves, P' is at most 2^3. Scales that are no numbers move
+//   nothing: p times such a scale carries the NaN to its own block. f16's 11
+//   bits reach down to 2^-16 of the largest product, its last one to 2^-26.
+//   ref and E move only when a tile breaks one of the two bounds, so a tile needs
+//   no maximum across lanes, only a vote.
 #pragma once
 
 #include <math.h>
@@ -57,21 +66,25 @@ namespace sa {
 
 template <int D>
 struct DecodeI4Cfg {
-  static constexpr int NCW = 16;                // consumer warps, 32 rows of a stage each
+  // Consumer warps, 32 rows of a stage each. d = 128 holds 8 accumulators and 8
+  // fragment words a block of four blocks: 12 warps of 144 registers (16 sequences
+  // of 16,384 rows: 71.8 us) rather than 16 of 104, which spill (103). d = 64 the
+  // other way round: 16 sequences of 65,536 rows 137 us with 16 warps, 150 with 12.
+  static constexpr int NCW = D == 128 ? 12 : 16;
   static constexpr int UNIT = 128;              // rows that shares count in
   static constexpr int R = 32 * NCW;            // rows per stage
   static constexpr int NB = D / kI4Block;       // blocks per row
   static constexpr int ROWB = D / 2;            // code bytes per row
   static constexpr uint32_t STAGE_BYTES = R * ROWB;
   static constexpr uint32_t SC_BYTES = R * NB * 2;   // K (or V) scales of one stage
-  static constexpr int NS = (D == 64) ? 5 : (D == 96 ? 3 : 2);
+  static constexpr int NS = (D == 64) ? 5 : 3;
   static constexpr uint32_t STAGE_TX = 2 * (STAGE_BYTES + SC_BYTES);
-  // five warpgroups: four of consumers, one of the producer and the three
-  // warps beside it, which gives registers to the others (640 * 96 at launch,
-  // 512 * 104 + 128 * 64 after)
+  // warpgroups of consumers, and one of the producer and the three warps beside
+  // it, which gives registers to the others (640 * 96 at launch, 512 * 104 + 128
+  // * 64 after; d = 128: 512 * 128, 384 * 144 + 128 * 64)
   static constexpr int NUM_THREADS = 32 * (NCW + 4);
   static constexpr int HELPERS = 96;
-  static constexpr int REGS_CONSUMER = 104, REGS_PRODUCER = 64;
+  static constexpr int REGS_CONSUMER = D == 128 ? 144 : 104, REGS_PRODUCER = 64;
   // K codes of the stages, then a tile of 32 rows for the new row (row 0
   // valid); the same of V; scales likewise ([R][NB] bf16 a stage)
   static constexpr uint32_t XTILE = (32 * ROWB + 1023) / 1024 * 1024;
@@ -189,30 +202,84 @@ __device__ __forceinline__ float i4_scale(const uint32_t* w, int blk) {
 }
 
 // What a consumer warp keeps of its (b, g). Of heads 2 (lane % 4) + {0, 1}: the
-// score scale hs and 1 / hs, what the sums are relative to (ref, see the head of this
-// file; ref = m + er) and the unscaled score thr = (m + 8) / hs that moves it;
-// the running sum l and those of P' per block ps (both over this lane's keys).
-// qf: the query fragments, qo: the offset's. lim: 2^(E + 1) as a bf16 pair, er =
-// E - 6. o[blk][i]: the accumulators of d = 32 blk + 4 (lane / 4) + 2 i + {0, 1}
-// (fragment rows g and g + 8, the latter times 16), offset included, times 2^-24.
+// score scale hs, ref (see the head of this file; 0 while no key has been seen) and
+// the unscaled score thr = (ref + 8) / hs that moves it (-inf while none has); the
+// running sum l (over this lane's keys), and for each block f and the sum of P',
+// ps. qf: the query fragments, qo: the offset's. lim: the blocks' 2^(E + 1), the
+// lesser of the two heads', as bf16 pairs like the scales. o[blk][i]: the
+// accumulators of d = 32 blk + 4 (lane / 4) + 2 i + {0, 1} (fragment rows g and g +
+// 8, the latter times 16), offset included, times f 2^-24.
 template <int D>
 struct I4State {
   static constexpr int NB = D / kI4Block;
   uint32_t qf[NB][4];
   uint32_t qo[2];
-  uint32_t lim;
-  float er, hs[2], rhs[2], m[2], ref[2], thr[2], l[2];
-  float ps[NB][2], o[NB][2][4];
+  uint32_t lim[(NB + 1) / 2];
+  float hs[2], ref[2], thr[2], l[2];
+  float f[NB][2], ps[NB][2], o[NB][2][4];
 };
 
-// lim for scales whose magnitudes (bf16 pairs) are at most mag in any lane. E
-// is kept within [-90, 125], so that sums of weights stay in range whatever
-// the scales. (Rare, so out of the tile's way.)
-__device__ __noinline__ uint32_t i4_raise(uint32_t mag) {
-  const uint32_t mx = __reduce_max_sync(0xffffffffu, max(mag & 0xFFFFu, mag >> 16));
-  const int e = (int)(mx >> 7) - 127;
-  const uint32_t top = (uint32_t)((e < -90 ? -90 : (e > 125 ? 125 : e)) + 128) << 7;   // 2^(e + 1)
-  return top | top << 16;
+// E within [-120, 126], so that f and 1 / f are normal numbers.
+constexpr int kI4MinE = -120, kI4MaxE = 126;
+
+// The largest of x over the lanes with the same heads.
+__device__ __forceinline__ float i4_max8(float x) {
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+}
+
+// ref and E after a tile that broke one of the bounds: s its scores, mx their
+// largest in this lane, sw its scales of V. E is what the tile's products ask
+// for, or what it was less the rise of ref.
+template <int D>
+__device__ __forceinline__ void i4_move(I4State<D>& z, const float (&s)[2][4], const float (&mx)[2],
+                                        const uint32_t (&sw)[4][(D / 32 + 1) / 2]) {
+  constexpr int NB = D / 32;
+  float p[4][2], down[2];   // down: log2 of what becomes of the sums so far
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const float x = i4_max8(mx[e]) * z.hs[e];
+    const bool empty = z.thr[e] == -INFINITY;
+    const float m = empty ? x : fmaxf(z.ref[e], x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    down[e] = empty ? 0.f : z.ref[e] - ref;
+    z.ref[e] = ref;
+    z.thr[e] = __fdividef(m + 8.f, z.hs[e]);
+    z.l[e] *= ex2(down[e]);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) p[c][e] = ex2(fmaf(s[c >> 1][2 * (c & 1) + e], z.hs[e], -ref));
+  }
+#pragma unroll
+  for (int blk = 0; blk < NB; ++blk) {
+    float w[2] = {};   // the largest products, of which the upper halves go across the lanes
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float v = fabsf(i4_scale(sw[c], blk));
+      w[0] = fmaxf(w[0], p[c][0] * v);   // (a NaN counts for nothing)
+      w[1] = fmaxf(w[1], p[c][1] * v);
+    }
+    uint32_t top = __byte_perm(__float_as_uint(w[0]), __float_as_uint(w[1]), 0x7632);
+#pragma unroll
+    for (int i = 4; i < 32; i <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, i));
+    int E[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int asked = (int)(top >> (16 * e + 7) & 0xFFu) - 123;
+      const int was = 133 - (int)(__float_as_uint(z.f[blk][e]) >> 23);
+      E[e] = min(max(max(asked, was + __float2int_rn(fmaxf(down[e], -512.f))), kI4MinE), kI4MaxE);
+      const float al = ex2(down[e] + (float)(was - E[e]));
+      z.f[blk][e] = __uint_as_float((uint32_t)(133 - E[e]) << 23);
+      z.ps[blk][e] *= al;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        z.o[blk][i][e] *= al;
+        z.o[blk][i][2 + e] *= al;
+      }
+    }
+    const uint32_t lim = (uint32_t)(min(E[0], E[1]) + 128) << 7;
+    z.lim[blk >> 1] = (blk & 1) ? z.lim[blk >> 1] | lim << 16 : lim;
+  }
 }
 
 // One warp's 32 keys of a stage: K codes at kst plus this lane's offsets
@@ -259,15 +326,14 @@ __device__ __forceinline__ void decode_tile_i4(uint32_t kst, const uint32_t (&of
       s[j][3] = fmaf(a[3], k1, s[j][3]);
     }
   }
-  // the scales of V: E over them all
-  uint32_t mag = 0;
+  uint32_t mag[NW] = {};   // the largest |scale_v| of each block
   i4_tile_scales<NB, VS>(ksc, sw);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
       if (MASK && !ok[c]) sw[c][i] = 0;   // a row never written holds anything
-      mag = __vmaxu2(mag, sw[c][i] & 0x7FFF7FFFu);
+      mag[i] = __vmaxu2(mag[i], sw[c][i] & 0x7FFF7FFFu);
     }
   }
   float mx[2];
@@ -280,32 +346,10 @@ __device__ __forceinline__ void decode_tile_i4(uint32_t kst, const uint32_t (&of
     }
     mx[e] = fmaxf(max3f(s[0][e], s[0][2 + e], s[1][e]), s[1][2 + e]);
   }
-  if (__any_sync(0xffffffffu, mx[0] > z.thr[0] || mx[1] > z.thr[1] || __vmaxu2(mag, z.lim) != z.lim)) {
-    z.lim = i4_raise(__vmaxu2(mag, z.lim - 0x00010001u));
-    z.er = (float)((int)(z.lim >> 23) - 134);   // E - 6
+  bool move = mx[0] > z.thr[0] || mx[1] > z.thr[1];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float x = fmaxf(mx[e], __shfl_xor_sync(0xffffffffu, mx[e], 4));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-      x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-      const bool empty = z.m[e] == -INFINITY;   // no key so far
-      z.m[e] = fmaxf(z.m[e], x * z.hs[e]);
-      const float ref = z.m[e] == -INFINITY ? 0.f : z.m[e] + z.er;
-      const float al = empty ? 0.f : ex2(z.ref[e] - ref);
-      z.ref[e] = ref;
-      z.thr[e] = (z.m[e] + 8.f) * z.rhs[e];
-      z.l[e] *= al;
-#pragma unroll
-      for (int blk = 0; blk < NB; ++blk) {
-        z.ps[blk][e] *= al;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          z.o[blk][i][e] *= al;
-          z.o[blk][i][2 + e] *= al;
-        }
-      }
-    }
-  }
+  for (int i = 0; i < NW; ++i) move = move || __vmaxu2(mag[i], z.lim[i]) != z.lim[i];
+  if (__any_sync(0xffffffffu, move)) i4_move<D>(z, s, mx, sw);
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -319,11 +363,14 @@ __device__ __forceinline__ void decode_tile_i4(uint32_t kst, const uint32_t (&of
     ldmatrix_x4_trans_at<VC>(kst + off[blk], x);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      // (in this order: f times the scale of a row without weight may be infinite)
       const float v = i4_scale(sw[c], blk);
-      const float p0 = s[c >> 1][2 * (c & 1)] * v, p1 = s[c >> 1][2 * (c & 1) + 1] * v;
-      z.ps[blk][0] += p0;
-      z.ps[blk][1] += p1;
-      pb[c] = movmatrix_trans(pack_f16(p0, p1));
+      float p0 = s[c >> 1][2 * (c & 1)], p1 = s[c >> 1][2 * (c & 1) + 1];
+      mul2(p0, p1, v, v);
+      mul2(p0, p1, z.f[blk][0], z.f[blk][1]);
+      const uint32_t ph = pack_f16(p0, p1);
+      add_f16x2(z.ps[blk][0], z.ps[blk][1], ph);
+      pb[c] = movmatrix_trans(ph);
     }
 #pragma unroll
     for (int c = 0; c < 4; c += 2) {
@@ -422,18 +469,17 @@ __device__ __forceinline__ void i4_start(I4State<D>& z, const uint4* qw, const f
     z.qo[0] = t < 2 ? wp[0] : wp[1];
     z.qo[1] = t < 2 ? wp[2] : 0u;
   }
-  z.er = -96.f;   // E = -90
-  z.lim = 0x13001300u;   // 2^-89, twice
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     z.hs[e] = 2 * t + e < QM ? hs[2 * t + e] : 1.f;
-    z.rhs[e] = __fdividef(1.f, z.hs[e]);
-    z.m[e] = z.thr[e] = -INFINITY;
+    z.thr[e] = -INFINITY;
     z.ref[e] = 0.f;
     z.l[e] = 0.f;
   }
 #pragma unroll
   for (int blk = 0; blk < NB; ++blk) {
+    z.lim[blk >> 1] = (uint32_t)(kI4MinE + 128) * 0x00800080u;   // 2^(E + 1), twice
+    z.f[blk][0] = z.f[blk][1] = __uint_as_float((uint32_t)(133 - kI4MinE) << 23);
     z.ps[blk][0] = z.ps[blk][1] = 0.f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) z.o[blk][i][0] = z.o[blk][i][1] = z.o[blk][i][2] = z.o[blk][i][3] = 0.f;
@@ -455,16 +501,17 @@ __device__ __forceinline__ void i4_write_partial(const I4State<D>& z, float* rw,
   for (int e = 0; e < 2; ++e) {
     const float l = sum8(z.l[e]);
     if (r == 0) {
-      rw[2 * t + e] = z.m[e] == -INFINITY ? -INFINITY : z.ref[e];
+      rw[2 * t + e] = z.thr[e] == -INFINITY ? -INFINITY : z.ref[e];
       rw[8 + 2 * t + e] = l;
     }
 #pragma unroll
     for (int blk = 0; blk < NB; ++blk) {
       const float c = -8.f * sum8(z.ps[blk][e]);   // the codes' offset
+      const float unit = __uint_as_float((254u << 23) - __float_as_uint(z.f[blk][e]));   // 1 / f
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         *reinterpret_cast<float2*>(rw + 16 + (2 * t + e) * D + 32 * blk + 4 * r + 2 * i) =
-            make_float2(fmaf(z.o[blk][i][e], 0x1p24f, c), fmaf(z.o[blk][i][2 + e], 0x1p20f, c));
+            make_float2(fmaf(z.o[blk][i][e], 0x1p24f, c) * unit, fmaf(z.o[blk][i][2 + e], 0x1p20f, c) * unit);
     }
   }
 }

@@ -470,6 +470,13 @@ __device__ __forceinline__ void mul2(float& a0, float& a1, float b0, float b1) {
       : "+f"(a0), "+f"(a1)
       : "f"(b0), "f"(b1));
 }
+// (a0, a1) += the two halves of an f16 pair.
+__device__ __forceinline__ void add_f16x2(float& a0, float& a1, uint32_t h) {
+  asm("{\n\t.reg .f16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "add.f32.f16 %0, lo, %0;\n\tadd.f32.f16 %1, hi, %1;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "r"(h));
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
