@@ -971,7 +971,7 @@ __global__ void __launch_bounds__(288, 2)
 
   for (int it = 0;; ++it) {
     const int s = it % C::NS;
-    if (!mbar_wait(full_bar(s), (uint32_t)((it / C::NS) & 1))) { flag[0] = 1; break; }
+    if (!mbar_wait_warp(full_bar(s), (uint32_t)((it / C::NS) & 1))) { flag[0] = 1; break; }
     const long long pos0 = srow[s];
     if (pos0 < 0) break;   // the producer's end mark
     const long long row0 = pos0 + C::RW * warp;

@@ -795,7 +795,7 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
   for (int u = u0;; ++i) {
     const int bg0 = u / per * per;   // the pair's first unit
     const int end = min(u1, bg0 + per);
-    if (!flag[0] && !mbar_wait(q_bar(i), (uint32_t)((i >> 1) & 1))) flag[0] = 1;
+    if (!mbar_wait_warp(q_bar(i), (uint32_t)((i >> 1) & 1))) flag[0] = 1;
     I4State<D> z;
     i4_start<D>(z, reinterpret_cast<const uint4*>(q_buf(i)), reinterpret_cast<const float*>(q_buf(i) + C::Q_SUM),
                 reinterpret_cast<const float*>(q_buf(i) + C::Q_HS), QM, lane);
@@ -813,18 +813,18 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
     const int n_st = (k_end - k0 + C::R / C::UNIT - 1) / (C::R / C::UNIT);
     const int busy = ((rows + 31) / 32) % C::NCW;
     const bool new_row = end == bg0 + per && warp == (busy > 0 ? busy : i % C::NCW);
-    const int n_it = flag[0] ? 0 : n_st + (new_row ? 1 : 0);
+    const int n_it = __any_sync(0xffffffffu, flag[0]) ? 0 : n_st + (new_row ? 1 : 0);
     for (int j = 0; j < n_it; ++j) {
       // the new row's tile stands to V's as a stage does (off counts from the
       // stage's start: 32 rows are whole patterns of the swizzle)
       uint32_t kt = sbase + C::OFF_XK - (uint32_t)(32 * warp * C::ROWB), ks = sbase + C::OFF_XS;
       if (j < n_st) {
-        if (!mbar_wait(full_bar(slot), phase)) { flag[0] = 1; break; }
+        if (!mbar_wait_warp(full_bar(slot), phase)) { flag[0] = 1; break; }
         kt = sbase + C::OFF_K + slot * C::STAGE_BYTES;
         ks = sbase + C::OFF_KS + slot * C::SC_BYTES + (uint32_t)(32 * warp * NB * 2);
       } else {
         // (every pair of this CTA before this one ended here: use i of row_bar)
-        if (!mbar_wait(row_bar, (uint32_t)(i & 1))) { flag[0] = 1; break; }
+        if (!mbar_wait_warp(row_bar, (uint32_t)(i & 1))) { flag[0] = 1; break; }
         left = 1;
         skip = 0;
       }
@@ -846,7 +846,7 @@ __global__ void __launch_bounds__(DecodeI4Cfg<D>::NUM_THREADS, 1)
       }
     }
     // the last pair's partials are read
-    if (i > 0 && !mbar_wait(free_bar, (uint32_t)((i - 1) & 1))) flag[0] = 1;
+    if (i > 0 && !mbar_wait_warp(free_bar, (uint32_t)((i - 1) & 1))) flag[0] = 1;
     i4_write_partial<D>(z, reinterpret_cast<float*>(smem + C::OFF_RED) + warp * (C::RED_WARP / 4), lane);
     u = end;
     if (u == u1) break;

@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(384, 1)
   // timed-out wait.
   auto fetch = [&](int k, bool elected, int& pair, int& h, int& b, float& sink) -> int {
     const int sl = k & 3;
-    if (!mbar_wait(bar(BAR_IFULL + sl), (uint32_t)((k >> 2) & 1))) {
+    if (!mbar_wait_warp(bar(BAR_IFULL + sl), (uint32_t)((k >> 2) & 1))) {
       *abort_flag = 1;
       return sched.n_items;
     }
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(384, 1)
         const int t_lo = rt ? geo.a_lo[1] : geo.a_lo[0], t_hi = rt ? geo.a_hi[1] : geo.a_hi[0];
         const int full_lo = rt ? geo.f_lo[1] : geo.f_lo[0], full_hi = rt ? geo.f_hi[1] : geo.f_hi[0];
         for (int t = t_lo; t < t_hi; ++t) {
-          if (!mbar_wait(bar(BAR_SFULL + X), (uint32_t)(ntot & 1))) { ok = false; *abort_flag = 1; break; }
+          if (!mbar_wait_warp(bar(BAR_SFULL + X), (uint32_t)(ntot & 1))) { ok = false; *abort_flag = 1; break; }
           tc_fence_after();
           uint32_t sr[BN];
 #pragma unroll
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(384, 1)
           l += (l0 + l1) + (l2 + l3);
           // O_X and P_X are read by the previous PV_X until it completes.
           if (ntot > 0) {
-            if (!mbar_wait(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1))) { ok = false; *abort_flag = 1; break; }
+            if (!mbar_wait_warp(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1))) { ok = false; *abort_flag = 1; break; }
             tc_fence_after();
           }
           if (rescale) {
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(384, 1)
         if (PARTS && p.splits > 1) {
           // a part: O, the max and the sum as they are
           const long long at = (long long)item * 256 + 128 * rt + r;
-          if (ok && n > 0 && mbar_wait(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1)) && !*abort_flag) {
+          if (ok && n > 0 && mbar_wait_warp(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1)) && !*abort_flag) {
             tc_fence_after();
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
@@ -762,7 +762,7 @@ __global__ void __launch_bounds__(384, 1)
               *reinterpret_cast<uint4*>(p.part_o + at * D + c) = make_uint4(0, 0, 0, 0);
           }
           if (row_ok) p.part_ml[at] = make_float2(m, l);
-        } else if (ok && n > 0 && mbar_wait(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1)) && !*abort_flag) {
+        } else if (ok && n > 0 && mbar_wait_warp(bar(BAR_ODONE + X), (uint32_t)((ntot - 1) & 1)) && !*abort_flag) {
           tc_fence_after();
           const float inv_l = 1.0f / l;
 #pragma unroll
