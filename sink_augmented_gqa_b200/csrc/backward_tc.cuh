@@ -343,11 +343,11 @@ __global__ void __launch_bounds__(BkvCfg<D>::NUM_THREADS, 1)
           ok = false;
         }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        mma_commit(bar(BK_DRAIN));
-        mbar_wait_drain(bar(BK_DRAIN), 0);
-      }
+      if (!ok) *abort_flag = 1;
+      // always: where the last wait for these products ran out, only the waiting
+      // warps have seen it
+      mma_commit(bar(BK_DRAIN));
+      mbar_wait_drain(bar(BK_DRAIN), 0);
     }
   } else {
     // ------------------------------------------------------------ P^T, dS^T, dQ and the epilogue

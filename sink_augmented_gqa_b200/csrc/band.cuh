@@ -98,7 +98,7 @@ enum : int {
   BD_PFULL = 12,   // [2] pipeline X's 4 warps -> MMA X: P_X stored
   BD_ODONE = 14,   // [2] MMA X -> pipeline X: O_X = P_X V completed
   BD_EPI = 16,     // [2] pipeline X's 4 warps -> store thread: O staged in smem
-  BD_DRAIN = 18,   // [2] per MMA issuer, on abort
+  BD_DRAIN = 18,   // [2] per MMA issuer, at its end
   BD_TMEM_SLOT = 20,
   BD_ABORT_SLOT = 21,
 };
@@ -464,11 +464,11 @@ __global__ void __launch_bounds__(544, 1)
         mma_commit(bar(BD_ODONE + X));
         if (*abort_flag) { ok = false; break; }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        mma_commit(bar(BD_DRAIN + X));
-        mbar_wait_drain(bar(BD_DRAIN + X), 0);
-      }
+      if (!ok) *abort_flag = 1;
+      // always: where the last wait for these products ran out, only the waiting
+      // warps have seen it
+      mma_commit(bar(BD_DRAIN + X));
+      mbar_wait_drain(bar(BD_DRAIN + X), 0);
     }
     if (lane == 3) {
       // ------------------------------------------------------------ output stores

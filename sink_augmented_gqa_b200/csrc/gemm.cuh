@@ -80,7 +80,7 @@ enum : int {
   GB_ACC_EMPTY = 10,  // count 8: epilogue warps -> MMA: accumulator read
   GB_RMS_FULL = 12,   // count 64: RMS lanes -> epilogue: row scales of the tile
   GB_RMS_EMPTY = 14,  // count 8: epilogue warps -> RMS warps
-  GB_DRAIN = 16,      // MMA issuer, on abort
+  GB_DRAIN = 16,      // MMA issuer, at its end
   GB_TMEM_SLOT = 17,
   GB_ABORT_SLOT = 18,
 };
@@ -196,11 +196,11 @@ __global__ void __launch_bounds__(384, 1)
         mma_commit(bar(GB_ACC_FULL));
         if (*abort_flag) { ok = false; break; }
       }
-      if (!ok) {
-        *abort_flag = 1;
-        mma_commit(bar(GB_DRAIN));
-        mbar_wait_drain(bar(GB_DRAIN), 0);
-      }
+      if (!ok) *abort_flag = 1;
+      // always: where the last wait for these products ran out, only the waiting
+      // warps have seen it
+      mma_commit(bar(GB_DRAIN));
+      mbar_wait_drain(bar(GB_DRAIN), 0);
     }
   } else if (warp < 4) {
     // ------------------------------------------------------------ RMSNorm row scales

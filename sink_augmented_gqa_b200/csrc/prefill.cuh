@@ -122,7 +122,7 @@ enum : int {
   BAR_PFULL = 8,    // [2] softmax -> MMA: P_X stored (and O_X rescaled)
   BAR_ODONE = 10,   // [2] MMA -> softmax: PV_X completed
   BAR_OFREE = 12,   // [2] softmax -> MMA: the item's epilogue has read O_X
-  BAR_DRAIN = 14,   // [2] per MMA issuer, on abort
+  BAR_DRAIN = 14,   // [2] per MMA issuer, at its end
   BAR_KFULL = 16,   // [NS <= 4]
   BAR_KEMPTY = 20,  // [NS] count 2: MMA A and MMA B
   BAR_VFULL = 24,   // [NS]
@@ -569,12 +569,12 @@ __global__ void __launch_bounds__(384, 1)
         gt += geo.ntiles;
         ++j;
       }
-      if (!ok) {
-        *abort_flag = 1;
-        // Drain this issuer's tensor-core work before anything is released.
-        mma_commit(bar(BAR_DRAIN + X));
-        mbar_wait_drain(bar(BAR_DRAIN + X), 0);
-      }
+      if (!ok) *abort_flag = 1;
+      // Drain this issuer's tensor-core work before anything is released. (It is
+      // through by now, unless the last epilogue's wait for it ran out: then this
+      // issuer has seen nothing of that.)
+      mma_commit(bar(BAR_DRAIN + X));
+      mbar_wait_drain(bar(BAR_DRAIN + X), 0);
     }
   } else {
     // ------------------------------------------------------------ softmax / epilogue
