@@ -23,6 +23,7 @@
 #include "ptx.cuh"
 #include "quant_stage.cuh"
 #include "rope.cuh"
+#include "sched_slots.cuh"
 
 namespace {
 
@@ -341,35 +342,22 @@ sa_status set_smem_once(K kernel, uint32_t bytes, std::atomic<uint64_t>& done) {
 
 constexpr int kMaxDevices = 64;
 
-// Counter slots of the prefill kernel's dynamic schedule (g_prefill_sched:
-// one counter pair per slot, reset by the last CTA of the launch that used
-// it). Two launches in flight at once must never share a slot.
-//  * Launches made outside stream capture take slots [0, kEagerSchedSlots)
-//    round robin. Before one reuses a slot its stream waits for the event
-//    recorded after the slot's previous launch, so the two are ordered
-//    whatever streams they run on (normally that launch finished long ago
-//    and the wait costs nothing).
-//  * Launches captured into a CUDA graph cannot wait on work outside the
-//    capture; they take slots [kEagerSchedSlots, kPrefillSchedSlots) round
-//    robin, so a graph never shares a slot with an eager launch. Graph
-//    replays that overlap one another must not hold more than
-//    kGraphSchedSlots prefill launches between them.
-constexpr int kEagerSchedSlots = sa::kPrefillSchedSlots / 2;
-constexpr int kGraphSchedSlots = sa::kPrefillSchedSlots - kEagerSchedSlots;
-
-int sched_slot_of(uint64_t index, bool captured) {
-  return captured ? kEagerSchedSlots + (int)(index % kGraphSchedSlots) : (int)(index % kEagerSchedSlots);
-}
-
-struct SchedState {
-  std::mutex mu;
-  uint64_t eager_next = 0, graph_next = 0;
-  cudaEvent_t done[kEagerSchedSlots] = {};
+// The slots of the prefill kernel's work counters, per device.
+static_assert(sa::kEagerSchedSlots + sa::kGraphSchedSlots == sa::kPrefillSchedSlots, "counter pairs");
+struct CudaSchedApi {
+  using Status = sa_status;
+  using Stream = cudaStream_t;
+  using Event = cudaEvent_t;
+  static constexpr Status kOk = SA_OK;
+  static Status create(Event* ev) {
+    return cudaEventCreateWithFlags(ev, cudaEventDisableTiming) == cudaSuccess ? SA_OK : SA_ERR_CUDA;
+  }
+  static Status wait(Stream s, Event ev) { return cudaStreamWaitEvent(s, ev, 0) == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
+  static Status record(Event ev, Stream s) { return cudaEventRecord(ev, s) == cudaSuccess ? SA_OK : SA_ERR_CUDA; }
 };
-SchedState g_sched[kMaxDevices];
+sa::SchedSlots<CudaSchedApi> g_sched[kMaxDevices];
 
-// Runs launch(slot) with a schedule slot acquired as above; the slot counts
-// as used only if the launch succeeded.
+// Runs launch(slot) with a schedule slot of the current device.
 template <typename F>
 sa_status with_sched_slot(cudaStream_t s, F&& launch) {
   int dev = 0;
@@ -377,25 +365,7 @@ sa_status with_sched_slot(cudaStream_t s, F&& launch) {
   if (dev < 0 || dev >= kMaxDevices) return SA_ERR_INVALID_ARG;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return SA_ERR_CUDA;
-  SchedState& st = g_sched[dev];
-  std::lock_guard<std::mutex> lock(st.mu);
-  if (cs != cudaStreamCaptureStatusNone) {
-    const sa_status r = launch(sched_slot_of(st.graph_next, true));
-    if (r == SA_OK) ++st.graph_next;
-    return r;
-  }
-  const int slot = sched_slot_of(st.eager_next, false);
-  cudaEvent_t& ev = st.done[slot];
-  if (ev == nullptr) {
-    if (cudaEventCreateWithFlags(&ev, cudaEventDisableTiming) != cudaSuccess) return SA_ERR_CUDA;
-  } else if (cudaStreamWaitEvent(s, ev, 0) != cudaSuccess) {
-    return SA_ERR_CUDA;
-  }
-  const sa_status r = launch(slot);
-  if (r != SA_OK) return r;
-  if (cudaEventRecord(ev, s) != cudaSuccess) return SA_ERR_CUDA;
-  ++st.eager_next;
-  return SA_OK;
+  return g_sched[dev].run(s, cs != cudaStreamCaptureStatusNone, launch);
 }
 
 // Launches a kernel of 256 threads a block that waits for the kernel ahead of it
@@ -1593,7 +1563,7 @@ sa_status sa_set_prefill_events(void* before, void* after) {
 }
 
 int32_t sa_prefill_sched_slot(uint64_t index, int32_t captured) {
-  return sched_slot_of(index, captured != 0);
+  return sa::sched_slot_of(index, captured != 0);
 }
 
 sa_status sa_set_wait_limit(int64_t cycles) {
