@@ -108,6 +108,7 @@ EXPORTS = (
 )
 
 _lib = None
+_F32 = torch.float32
 
 
 def lib():
@@ -172,7 +173,10 @@ def _stream(t=None):
 
 def _raw_stream(t):
     """The current stream of t's device, which must be the current one, as a raw handle (no Stream object)."""
-    index = t.device.index
+    return _device_stream(t.device.index)
+
+
+def _device_stream(index):
     if index != torch._C._cuda_getDevice():
         raise ValueError(f"the tensors are on cuda:{index}, which is not the current device")
     return torch._C._cuda_getCurrentRawStream(index)
@@ -232,6 +236,7 @@ def rope_apply_qk(q, k, offset, cos, sin):
     n_kv = k.shape[2] if k is not None else 0
     qs = _strides(q) if q is not None else _I64x3(0, 0, 0)
     ks = _strides(k) if k is not None else _I64x3(0, 0, 0)
+    _check_tables(cos, sin, d, ref.get_device())
     _check(lib().sa_rope_apply_qk(_ptr(q), qs, _ptr(k), ks, B, T, n_q, n_kv, d, int(offset),
                                   _ptr(cos), _ptr(sin), cos.shape[0], _stream(ref)),
            "sa_rope_apply_qk")
@@ -269,6 +274,8 @@ class KVCache:
         assert tuple(self.v.shape) == shape
         assert self.k.dtype == dt and self.v.dtype == dt
         self.raw = _KVCache()
+        self.device_index = self.k.get_device()   # -1: host memory
+        assert self.v.get_device() == self.device_index
         self.fp8 = bool(fp8)
         self.int4 = bool(int4)
         if fp8 or int4:
@@ -278,6 +285,7 @@ class KVCache:
             self.v_scale = v_scale if v_scale is not None else torch.zeros(sshape, dtype=sdt, device=self.k.device)
             for t in (self.k_scale, self.v_scale):
                 assert tuple(t.shape) == sshape and t.dtype == sdt and t.is_contiguous()
+                assert t.get_device() == self.device_index
             name = "sa_kv_cache_init_fp8" if fp8 else "sa_kv_cache_init_int4"
             _check(getattr(lib(), name)(ctypes.byref(self.raw), _ptr(self.k), _ptr(self.v), _ptr(self.k_scale),
                                         _ptr(self.v_scale), B, cap, n_kv, d, int(ring)), name)
@@ -324,8 +332,10 @@ class KVCache:
         raw, shape = self.raw, k_rot.shape
         if v.shape != shape or shape != (raw.B, shape[1], raw.n_kv, raw.d):
             raise ValueError("k_rot and v must be [B, T, n_kv, d] with the cache's B, n_kv and d")
+        if k_rot.get_device() != self.device_index or v.get_device() != self.device_index:
+            raise ValueError("k_rot and v must be on the cache's device")
         _check(lib().sa_kv_append(ctypes.byref(self.raw), k_rot.data_ptr(), _I64x3(ks[0], ks[1], ks[2]), v.data_ptr(),
-                                  _I64x3(vs[0], vs[1], vs[2]), k_rot.shape[1], _raw_stream(self.k)), "sa_kv_append")
+                                  _I64x3(vs[0], vs[1], vs[2]), k_rot.shape[1], _device_stream(self.device_index)), "sa_kv_append")
 
     def read(self, start=0, stop=None, k_out=None, v_out=None):
         """kv_read: positions [start, stop) as bf16 rows (k, v) [B, T, n_kv, d]
@@ -342,13 +352,15 @@ class KVCache:
             vs = _view4("v_out", v_out)
         if (ks and k_out.shape != (B, T, H, d)) or (vs and v_out.shape != (B, T, H, d)):
             raise ValueError(f"k_out and v_out must be {(B, T, H, d)}")
+        if (ks and k_out.get_device() != self.device_index) or (vs and v_out.get_device() != self.device_index):
+            raise ValueError("k_out and v_out must be on the cache's device")
         dense = _I64x3(T * H * d, H * d, d)
         if ks is None:
             k_out = _empty4(B, T, H, d, self.k.device)
         if vs is None:
             v_out = torch.empty_like(k_out) if ks is None else _empty4(B, T, H, d, self.k.device)
         _check(lib().sa_kv_read(ctypes.byref(raw), start, T, k_out.data_ptr(), _I64x3(*ks[:3]) if ks else dense,
-                                v_out.data_ptr(), _I64x3(*vs[:3]) if vs else dense, _raw_stream(self.k)),
+                                v_out.data_ptr(), _I64x3(*vs[:3]) if vs else dense, _device_stream(self.device_index)),
                "sa_kv_read")
         return k_out, v_out
 
@@ -371,24 +383,58 @@ def _view4(name, t):
     return st
 
 
+def _check_f32(name, t, shape, dev):
+    """Raises unless t is a contiguous fp32 tensor of this shape on CUDA device dev."""
+    if t.dtype is not _F32 or t.get_device() != dev or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous fp32 tensor on the inputs' CUDA device")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def _check_tables(cos, sin, d, dev):
+    _check_f32("cos", cos, (cos.shape[0] if cos.dim() else 0, d // 2), dev)
+    _check_f32("sin", sin, cos.shape, dev)
+
+
+def _check_workspace(workspace, dev):
+    if not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous tensor on the inputs' CUDA device")
+
+
 def _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse):
     """sa_attn_args for one call, packed into this thread's reusable struct
     (the library reads it only during the call)."""
     qs, ks, vs, os_ = _view4("q", q), _view4("k", k), _view4("v", v), _view4("out", out)
-    raw, shape, kv = cache.raw, q.shape, k.shape
-    if v.shape != kv or out.shape != shape or kv != (shape[0], shape[1], raw.n_kv, shape[3]) or shape[3] != raw.d:
+    raw, dev = cache.raw, cache.device_index
+    B, T, n_q, d = shape = q.shape
+    if k.shape != (B, T, raw.n_kv, d) or v.shape != k.shape or out.shape != shape or d != raw.d:
         raise ValueError("k and v must be [B, T, n_kv, d] and out like q, with the cache's n_kv and d")
-    if sinks is not None and (sinks.dtype != torch.float32 or not sinks.is_contiguous()):
-        raise TypeError("sinks must be a contiguous fp32 CUDA tensor")
+    if not q.get_device() == k.get_device() == v.get_device() == out.get_device() == dev:
+        raise ValueError("the cache, q, k, v and out must be on one device")
+    # (written out: a decode step makes one call per layer, and four calls of _check_f32 take 1 us)
+    if sinks is not None and (sinks.dtype is not _F32 or sinks.get_device() != dev or sinks.shape != (n_q,)
+                              or not sinks.is_contiguous()):
+        _check_f32("sinks", sinks, (n_q,), dev)
+    if lse is not None and (lse.dtype is not _F32 or lse.get_device() != dev or lse.shape != (B, n_q, T)
+                            or not lse.is_contiguous()):
+        _check_f32("lse", lse, (B, n_q, T), dev)
+    max_pos = 0
+    if cos is not None:
+        table = cos.shape
+        max_pos = table[0]
+        if sin is not None and (cos.dtype is not _F32 or sin.dtype is not _F32 or table != (max_pos, d // 2) or
+                                sin.shape != table or not cos.is_contiguous() or not sin.is_contiguous() or
+                                not cos.get_device() == sin.get_device() == dev):
+            _check_tables(cos, sin, d, dev)
     a = getattr(_tls, "args", None)
     if a is None:
         a = _tls.args = _AttnArgs()
     struct.pack_into(_ATTN_FMT, a, 0,
                      q.data_ptr(), qs[0], qs[1], qs[2], k.data_ptr(), ks[0], ks[1], ks[2],
                      v.data_ptr(), vs[0], vs[1], vs[2], 0 if sinks is None else sinks.data_ptr(),
-                     shape[0], shape[1], shape[2], raw.offset, int(window), float(sm_scale),
+                     B, T, n_q, raw.offset, int(window), float(sm_scale),
                      1 if rope_fused else 0, 0 if cos is None else cos.data_ptr(),
-                     0 if sin is None else sin.data_ptr(), 0 if cos is None else cos.shape[0],
+                     0 if sin is None else sin.data_ptr(), max_pos,
                      out.data_ptr(), os_[0], os_[1], os_[2], 0 if lse is None else lse.data_ptr())
     return a
 
@@ -403,7 +449,8 @@ def attn_prefill(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=None, ro
     if return_lse and lse is None:
         lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
-    _check(lib().sa_attn_prefill(ctypes.byref(cache.raw), ctypes.byref(a), _raw_stream(q)), "sa_attn_prefill")
+    _check(lib().sa_attn_prefill(ctypes.byref(cache.raw), ctypes.byref(a), _device_stream(cache.device_index)),
+           "sa_attn_prefill")
     return (out, lse) if return_lse else out
 
 
@@ -420,15 +467,14 @@ def attn_prefill_quant(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=No
     B, T, n_q, d = q.shape
     if workspace is None:
         workspace = prefill_quant_workspace(cache, T, window)
-    elif not (workspace.is_cuda and workspace.is_contiguous()):
-        raise TypeError("workspace must be a contiguous CUDA tensor")
     if out is None:
         out = _empty_out(q)
     if return_lse and lse is None:
         lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
+    _check_workspace(workspace, cache.device_index)
     _check(lib().sa_attn_prefill_quant(ctypes.byref(cache.raw), ctypes.byref(a), workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), _raw_stream(q)),
+                                       workspace.nbytes, _device_stream(cache.device_index)),
            "sa_attn_prefill_quant")
     return (out, lse) if return_lse else out
 
@@ -453,8 +499,9 @@ def attn_decode(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=None, rop
     if return_lse and lse is None:
         lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
+    _check_workspace(workspace, cache.device_index)
     _check(lib().sa_attn_decode(ctypes.byref(cache.raw), ctypes.byref(a), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _raw_stream(q)),
+                                workspace.nbytes, _device_stream(cache.device_index)),
            "sa_attn_decode")
     return (out, lse) if return_lse else out
 
@@ -507,6 +554,13 @@ def attn_backward(q, k, v, out, d_out, lse, sinks, window, sm_scale, workspace=N
     n_kv = k.shape[2]
     for n, t in (("q", q), ("k", k), ("v", v), ("out", out), ("d_out", d_out)):
         _require_bf16_cuda(n, t)
+    if not (q.shape == out.shape == d_out.shape and k.shape == v.shape == (B, T, n_kv, d)):
+        raise ValueError("q, out and d_out must be [B, T, n_q, d], k and v [B, T, n_kv, d]")
+    if any(t.get_device() != q.get_device() for t in (k, v, out, d_out)):
+        raise ValueError("q, k, v, out and d_out must be on one device")
+    _check_f32("lse", lse, (B, n_q, T), q.get_device())
+    if sinks is not None:
+        _check_f32("sinks", sinks, (n_q,), q.get_device())
     dev = q.device
     dq = torch.empty((B, T, n_q, d), dtype=torch.float32, device=dev)
     dk = torch.empty((B, T, n_kv, d), dtype=torch.float32, device=dev)
@@ -515,6 +569,7 @@ def attn_backward(q, k, v, out, d_out, lse, sinks, window, sm_scale, workspace=N
     if workspace is None:
         nb = lib().sa_attn_backward_workspace_size(B, T, n_q)
         workspace = torch.empty(nb, dtype=torch.uint8, device=dev)
+    _check_workspace(workspace, q.get_device())
     a = _BwdArgs()
     a.q, a.q_strides = q.data_ptr(), _strides(q)
     a.k, a.k_strides = k.data_ptr(), _strides(k)
@@ -544,7 +599,7 @@ def attn_decode_static(cache, q, k, v, sinks, window, sm_scale, cos=None, sin=No
     if return_lse and lse is None:
         lse = _empty_lse(B, n_q, T, q.device)
     a = _args(cache, q, k, v, sinks, window, sm_scale, cos, sin, rope_fused, out, lse)
-    _check(lib().sa_attn_decode_static(ctypes.byref(cache.raw), ctypes.byref(a), _raw_stream(q)),
+    _check(lib().sa_attn_decode_static(ctypes.byref(cache.raw), ctypes.byref(a), _device_stream(cache.device_index)),
            "sa_attn_decode_static")
     return (out, lse) if return_lse else out
 
