@@ -216,7 +216,8 @@ __device__ __forceinline__ void band_softmax(const BandParams& p, uint8_t* smem,
         tmem_st16(s_tm + c0, v);
       }
     };
-    // pass 1: this half's row maximum, two chunks per TMEM round trip
+    // pass 1: this half's row maximum (NaN where a score is: the polynomial
+    // exponentials would pass over one), two chunks per TMEM round trip
     float mx = -INFINITY;
 #pragma unroll
     for (int jj = 0; jj < C::NMAX / 32; jj += 2) {
@@ -230,18 +231,18 @@ __device__ __forceinline__ void band_softmax(const BandParams& p, uint8_t* smem,
         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 16; c += 4) {
-          m0 = max3f(m0, __uint_as_float(v0[c]), __uint_as_float(v0[c + 1]));
-          m1 = max3f(m1, __uint_as_float(v0[c + 2]), __uint_as_float(v0[c + 3]));
+          m0 = max3_nan(m0, __uint_as_float(v0[c]), __uint_as_float(v0[c + 1]));
+          m1 = max3_nan(m1, __uint_as_float(v0[c + 2]), __uint_as_float(v0[c + 3]));
         }
         if (two) {
           mask16(v1, j0 + jj + 1);
 #pragma unroll
           for (int c = 0; c < 16; c += 4) {
-            m0 = max3f(m0, __uint_as_float(v1[c]), __uint_as_float(v1[c + 1]));
-            m1 = max3f(m1, __uint_as_float(v1[c + 2]), __uint_as_float(v1[c + 3]));
+            m0 = max3_nan(m0, __uint_as_float(v1[c]), __uint_as_float(v1[c + 1]));
+            m1 = max3_nan(m1, __uint_as_float(v1[c + 2]), __uint_as_float(v1[c + 3]));
           }
         }
-        mx = fmaxf(mx, fmaxf(m0, m1));
+        mx = max_nan(mx, max_nan(m0, m1));
       }
     }
     // trade maxima with the other half of the row; all of the pipeline
@@ -252,10 +253,10 @@ __device__ __forceinline__ void band_softmax(const BandParams& p, uint8_t* smem,
     if (fail) *abort_flag = 1;
     if (named_bar_or(pipe_bar, 256, fail || *abort_flag)) break;
     tc_fence_after();
-    mx = fmaxf(mx, __uint_as_float(tmem_ld1(x_tm + (1 - hf))));
+    mx = max_nan(mx, __uint_as_float(tmem_ld1(x_tm + (1 - hf))));
     tmem_wait_ld();
     // the row's maximum in log2 units, the sink included (scale > 0)
-    const float mrow = fmaxf(sink2, mx * scale);
+    const float mrow = max_nan(sink2, mx * scale);
     const float neg = (mrow == -INFINITY) ? 0.f : -mrow;
     // pass 2: exp2, the partial sum, P. P of chunk j (8 bf16-pair columns)
     // goes over the first half of S chunk j's own columns, already read.

@@ -652,18 +652,20 @@ __global__ void __launch_bounds__(384, 1)
                 if (c < cmin) sr[c] = __float_as_uint(-INFINITY);
             }
           }
-          // raw row max (scale > 0, so max(s * scale) = scale * max(s))
+          // raw row max (scale > 0, so max(s * scale) = scale * max(s)), NaN where a
+          // score is: the polynomial exponentials below would pass over one
           float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
           for (int c = 0; c < BN; c += 8) {
-            m0 = max3f(m0, __uint_as_float(sr[c + 0]), __uint_as_float(sr[c + 1]));
-            m1 = max3f(m1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
-            m2 = max3f(m2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
-            m3 = max3f(m3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
+            m0 = max3_nan(m0, __uint_as_float(sr[c + 0]), __uint_as_float(sr[c + 1]));
+            m1 = max3_nan(m1, __uint_as_float(sr[c + 2]), __uint_as_float(sr[c + 3]));
+            m2 = max3_nan(m2, __uint_as_float(sr[c + 4]), __uint_as_float(sr[c + 5]));
+            m3 = max3_nan(m3, __uint_as_float(sr[c + 6]), __uint_as_float(sr[c + 7]));
           }
-          const float mx = fmaxf(max3f(m0, m1, m2), m3) * scale;
-          const float m_new = fmaxf(m, mx);
-          const bool need = m_new > m + 8.0f;
+          const float mx = max_nan(max3_nan(m0, m1, m2), m3) * scale;
+          const float m_new = max_nan(m, mx);
+          // (idle rows of a packed tile hold anything)
+          const bool need = !(m_new <= m + 8.0f) && (!PARTS || row_ok);
           // O_X is rescaled by f later, once the previous PV_X has landed.
           const bool rescale = __any_sync(0xffffffffu, need) && n > 0;
           float f = 1.0f;
