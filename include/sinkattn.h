@@ -377,8 +377,11 @@ size_t sa_attn_prefill_quant_workspace_size(const sa_kv_cache* cache, int32_t T,
  * value.
  * workspace: device memory of at least sa_attn_decode_workspace_size()
  *   bytes, caller-owned, ZERO-FILLED before its first use; the kernel leaves
- *   it zeroed again on completion. Calls that share a workspace must not
- *   overlap on the device (order them on one stream).
+ *   the part that must be zero so on completion. Calls that share a workspace
+ *   must not overlap on the device (order them on one stream); they may differ
+ *   in shape and cache format, as layers of a model do, where B * n_kv is at
+ *   most 4,096 in all of them (else zero-fill it between two values of
+ *   B * n_kv).
  */
 sa_status sa_attn_decode(sa_kv_cache* cache, const sa_attn_args* args, void* workspace,
                          size_t workspace_bytes, sa_stream_t stream);
@@ -395,8 +398,9 @@ size_t sa_attn_decode_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32
  *
  * Same operation, arguments and results as sa_attn_decode, but the split
  * scratch lives in a fixed array inside the library (a file-scope
- * __device__ array of SA_DECODE_STATIC_SCRATCH_BYTES bytes, which every GPU
- * that loads the library holds until the process exits). No call allocates:
+ * __device__ array of SA_DECODE_STATIC_SCRATCH_BYTES bytes and 32 KB of
+ * counters, which every GPU that loads the library holds until the process
+ * exits). No call allocates:
  * no cudaMalloc, cudaFree or allocating library routine.
  * - The first call on a device (with that device current) looks up the
  *   array's device address and zeroes it once; make that first call before

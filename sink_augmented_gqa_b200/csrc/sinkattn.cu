@@ -620,12 +620,20 @@ int decode_splits(int B, int n_kv, long long n_cache, long long stage) {
 }
 
 // Workspace layout: split tickets [B*n_kv] then dynamic-stage counters
-// [B*n_kv], int32 (256-byte padded), then one fp32 record per (b, g, split):
-// O [q_mult][d], m [q_mult], l [q_mult], padded to a multiple of 16 bytes
-// (the merge brings records in by bulk copy).
+// [B*n_kv], int32, then one fp32 record per (b, g, split): O [q_mult][d],
+// m [q_mult], l [q_mult], padded to a multiple of 16 bytes (the merge brings
+// records in by bulk copy). A call leaves the counters at zero, the records as
+// they are: these start at the same offset for every B * n_kv up to
+// kDecodeCounterBytes / 8, so that no call finds another shape's records in
+// its counters.
+constexpr size_t kDecodeCounterBytes = 32768;
+
 int decode_rec_floats(int q_mult, int d) { return q_mult * d + (2 * q_mult + 3) / 4 * 4; }
 
-size_t decode_cnt_bytes(int B, int n_kv) { return (((size_t)B * n_kv * 8) + 255) / 256 * 256; }
+size_t decode_cnt_bytes(int B, int n_kv) {
+  const size_t used = ((size_t)B * n_kv * 8 + 255) / 256 * 256;
+  return used > kDecodeCounterBytes ? used : kDecodeCounterBytes;
+}
 
 size_t decode_ws_bytes(int B, int n_kv, int q_mult, int d, long long records) {
   return decode_cnt_bytes(B, n_kv) + (size_t)records * decode_rec_floats(q_mult, d) * 4;
@@ -1063,7 +1071,9 @@ sa_status launch_quant_stage(const sa_kv_cache* c, const sa_kv_cache* w, const s
 // Scratch of sa_attn_decode_static: one fixed array per device, its device
 // address looked up once per device (host code may not use the symbol itself
 // as an address).
-static __device__ __align__(256) uint8_t g_decode_scratch[SA_DECODE_STATIC_SCRATCH_BYTES];
+// (the records', and the counters ahead of them)
+constexpr size_t kStaticScratchBytes = SA_DECODE_STATIC_SCRATCH_BYTES + kDecodeCounterBytes;
+static __device__ __align__(256) uint8_t g_decode_scratch[kStaticScratchBytes];
 std::mutex g_scratch_mu;
 void* g_scratch_ptr[kMaxDevices] = {};
 
@@ -1076,7 +1086,7 @@ sa_status static_scratch(void** out) {
     void* ptr = nullptr;
     if (cudaGetSymbolAddress(&ptr, g_decode_scratch) != cudaSuccess || ptr == nullptr) return SA_ERR_CUDA;
     // the split counters must start at zero (each call leaves them at zero)
-    if (cudaMemset(ptr, 0, SA_DECODE_STATIC_SCRATCH_BYTES) != cudaSuccess) return SA_ERR_CUDA;
+    if (cudaMemset(ptr, 0, kStaticScratchBytes) != cudaSuccess) return SA_ERR_CUDA;
     if (cudaDeviceSynchronize() != cudaSuccess) return SA_ERR_CUDA;
     g_scratch_ptr[dev] = ptr;
   }
@@ -1464,12 +1474,12 @@ sa_status sa_attn_decode_static(sa_kv_cache* cache, const sa_attn_args* a, sa_st
   if (q_mult > 8) return SA_ERR_SHAPE;
   const long long records = plan_decode(cache, a).records;   // of the split the launch will use
   if (records > 0 &&
-      decode_ws_bytes(a->B, cache->n_kv, q_mult, cache->d, records) > SA_DECODE_STATIC_SCRATCH_BYTES)
+      decode_ws_bytes(a->B, cache->n_kv, q_mult, cache->d, records) > kStaticScratchBytes)
     return SA_ERR_WORKSPACE;
   void* scratch = nullptr;
   st = static_scratch(&scratch);
   if (st != SA_OK) return st;
-  return sa_attn_decode(cache, a, scratch, SA_DECODE_STATIC_SCRATCH_BYTES, stream);
+  return sa_attn_decode(cache, a, scratch, kStaticScratchBytes, stream);
 }
 
 size_t sa_attn_decode_workspace_size(int32_t B, int32_t n_q, int32_t n_kv, int32_t d) {
