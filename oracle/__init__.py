@@ -32,8 +32,9 @@ Modules, each citing the passage it restates:
                    with dequantisation; the format is a reading, pinned by
                    ``tests/test_oracle_fp8.py``).
 * ``int4``      -- 4-bit rows with one bf16 scale per 32 elements: quantise
-                   and dequantise (same source; the format is this library's
-                   own, pinned by ``tests/test_oracle_int4.py``).
+                   and dequantise (same source; the codes are the published
+                   Q4_0 scheme's, the scale's bits this library's own; pinned
+                   by ``tests/test_oracle_int4.py``).
 
 Parity status: every function here is pinned by ``tests/test_oracle_pins.py``
 except the two readings listed there as "parity unpinned" (the RoPE pair

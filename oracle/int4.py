@@ -3,8 +3,10 @@
 TEST INFRASTRUCTURE (see ``oracle/__init__.py``).
 
 The MoE-Xtend README lists quantisation-aware long-context runs, with KV and
-its dequantisation first because decode is bandwidth bound ("ROADMAP"); the
-format is this library's own:
+its dequantisation first because decode is bandwidth bound ("ROADMAP"). The
+codes are those of the published Q4_0 scheme (the ``u`` below over blocks of
+32 with ``s = -m / 8``); the scale's 5 bits, the tie of ``m`` and ``-m``, zeros
+and NaNs are this library's own:
 
 * blocks of 32 consecutive elements of a bf16 row; ``m`` is the block's element
   of largest magnitude (the positive one where ``m`` and ``-m`` both occur);
@@ -19,10 +21,6 @@ Two codes share a byte, the even element in the low half.
 """
 
 import numpy as np
-
-from .attention import sink_attention
-from .bf16 import round_bf16
-from .rope import rotate_bsh
 
 BLOCK = 32
 SMALLEST = 2.0 ** -120
@@ -71,21 +69,6 @@ def unpack(packed):
 def stored_rows(x):
     """What the rows ``x`` stand for once they are in the cache."""
     return dequantize_rows(*quantize_rows(x))
-
-
-def attend_step_int4(cache, q, k, v, sinks, window, sm_scale, cos_tab, sin_tab, rope_fused=True):
-    """One call of the hot path on a quantised cache: as
-    ``attention.attend_step``, except that the call's rows are stored and
-    attended quantised. ``cache`` is an fp64 ``kvcache.KVCache`` holding
-    dequantised rows."""
-    off = cache.offset
-    if rope_fused:
-        q_rot = rotate_bsh(q, off, cos_tab, sin_tab)
-        k_rot = rotate_bsh(k, off, cos_tab, sin_tab)
-    else:
-        q_rot, k_rot = round_bf16(q), round_bf16(k)
-    cache.append(stored_rows(k_rot), stored_rows(round_bf16(v)))
-    return sink_attention(q_rot, cache.K, cache.V, sinks, off, window, sm_scale)
 
 
 def kv_bytes_int4(L, B, T, H_kv, d):

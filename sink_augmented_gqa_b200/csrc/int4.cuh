@@ -2,15 +2,18 @@
 // 32 elements, 4.5 bits an element, and the kernels that write such rows and
 // read quantised rows back.
 //
-// A block of 32 bf16 values x with m its element of largest magnitude (the
-// positive one of two opposite ones) is kept as
+// The codes are those of the published Q4_0 scheme (blocks of 32, the step an
+// eighth of the largest element with its sign turned); the scale's 5 bits, the
+// tie, zeros and NaNs are this library's own. A block of 32 bf16 values x with m its
+// element of largest magnitude (the positive one of two opposite ones) is kept as
 //   s = -m / 8 rounded to 5 significant bits (nearest, ties to even), bf16
 //   u = min(15, floor(x / s + 8.5)),  0 <= u <= 15
 // and stands for s (u - 8). The scale carries the sign that sends m to the
 // code 0, the one end of the range that has a step more: with the step
 // |m| / 8 instead of |m| / 7 the error of the other elements is an eighth
-// smaller, and only elements beyond 7.5 / 8 of m with the opposite sign are
-// clipped (by less than a step). s has 5 significant bits and u - 8 at most
+// smaller, and only elements of the opposite sign beyond 7.5 steps (from 7.5 / 8.25
+// of m on, where s is rounded down furthest) are clipped, by a step and a quarter at
+// most. s has 5 significant bits and u - 8 at most
 // 3, so every stored value is exactly a bf16 number: all readers see the
 // same rows (decode multiplies codes and scales apart, the read-back returns
 // bf16), and rows read back and appended again give the same codes, because
