@@ -252,8 +252,11 @@ sa_status sa_kv_cache_init_fp8(sa_kv_cache* cache, void* k, void* v, void* k_sca
  * at most |m|/15 for |x| <= 7/8 |m| or x of m's sign, and at most |m|/6
  * otherwise. Rows read back (sa_kv_read) and appended to an INT4 cache again
  * give the same codes. A block whose m is under 2^-120 is kept as zeros; a
- * block that holds an infinity or a NaN reads as 32 NaNs. Values of V beyond
- * 2^100 may overflow the sums of sa_attn_decode.
+ * block that holds an infinity or a NaN reads as 32 NaNs, and in V makes those
+ * 32 outputs NaN, no others. Rows and blocks of V may lie any number of powers of
+ * two apart: sa_attn_decode holds each head and block to about 2^-11 of its sum
+ * of weights times |v| (before the output's own rounding). Values of V beyond
+ * 2^100 may overflow its sums.
  * Buffers of a ring cache, scales included, must be zeroed before first use.
  */
 sa_status sa_kv_cache_init_int4(sa_kv_cache* cache, void* k, void* v, void* k_scale, void* v_scale,
@@ -340,10 +343,16 @@ sa_status sa_attn_prefill(sa_kv_cache* cache, const sa_attn_args* args, sa_strea
  *   16-byte aligned, contents irrelevant: the rows that the call attends as
  *   bf16 (reading them back once costs a fraction of the attention over them
  *   for all heads and rows), and partial sums where a call has too few rows
- *   and heads to give every SM work and its keys are shared out. Calls that share a workspace must not overlap on
- *   the device; it may be shared by all layers of a model.
+ *   and heads to give every SM work and its keys are shared out. Calls that
+ *   share a workspace must not overlap on the device; it may be shared by all
+ *   layers of a model.
  * `out` may be `q` itself; else it overlaps no input, the cache nor the
  * workspace.
+ * A key that reads back with a NaN makes the rows that attend it NaN. A value of
+ * V that is not finite makes its element NaN in the rows that attend it, and also
+ * in rows of the call that mask it (a later position, or one behind the band) but
+ * share a tile of keys with it: zero times infinity. The same goes for
+ * sa_attn_prefill.
  * Schedule counters and graph capture as for sa_attn_prefill.
  * SA_ERR_UNSUPPORTED on a bf16 cache (sa_attn_prefill); SA_ERR_WORKSPACE.
  */
@@ -370,11 +379,12 @@ size_t sa_attn_prefill_quant_workspace_size(const sa_kv_cache* cache, int32_t T,
  * attended quantised; codes enter both products as integers, queries the QK
  * product in f16 after an exact per-head power-of-two scaling, the weights
  * times the block scales of V the PV product as f16.
- * The rows are shared out among the CTAs of each (sequence, KV head) at run
- * time (the CTAs that stream faster take more), so the fp32 partial sums are
- * grouped differently from call to call: two identical calls can differ in
- * the last bit of an output, each within the same rounding of the exact
- * value.
+ * On bf16 and FP8 caches the rows are shared out among the CTAs of each
+ * (sequence, KV head) at run time (the CTAs that stream faster take more), so
+ * the fp32 partial sums are grouped differently from call to call: two
+ * identical calls can differ in the last bit of an output, each within the same
+ * rounding of the exact value. On an INT4 cache the shares follow from the
+ * call's shape and are joined in order: identical calls give identical bits.
  * workspace: device memory of at least sa_attn_decode_workspace_size()
  *   bytes, caller-owned, ZERO-FILLED before its first use; the kernel leaves
  *   the part that must be zero so on completion. Calls that share a workspace

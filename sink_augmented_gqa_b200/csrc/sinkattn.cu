@@ -407,8 +407,8 @@ struct PrefillSplit {
   long long items;   // parts counted
 };
 constexpr int kSplitTiles = 2;     // key tiles of a part, at least
-// Items of a split launch, at most: two waves, so that items which half fill a
-// second one can be cut finer (300 rows of 64 / 8 heads behind 16,384: 80 items of
+// Items of a split launch, at most: what the workspace holds, a little over two waves
+// of 148 SMs, so that items which half fill a second one can be cut finer (300 rows of 64 / 8 heads behind 16,384: 80 items of
 // 8 heads in 3 parts, 172 us, against 214 of 128 whole ones).
 constexpr int kSplitSlots = 320;
 

@@ -335,7 +335,8 @@ class KVCache:
         if k_rot.get_device() != self.device_index or v.get_device() != self.device_index:
             raise ValueError("k_rot and v must be on the cache's device")
         _check(lib().sa_kv_append(ctypes.byref(self.raw), k_rot.data_ptr(), _I64x3(ks[0], ks[1], ks[2]), v.data_ptr(),
-                                  _I64x3(vs[0], vs[1], vs[2]), k_rot.shape[1], _device_stream(self.device_index)), "sa_kv_append")
+                                  _I64x3(vs[0], vs[1], vs[2]), shape[1], _device_stream(self.device_index)),
+               "sa_kv_append")
 
     def read(self, start=0, stop=None, k_out=None, v_out=None):
         """kv_read: positions [start, stop) as bf16 rows (k, v) [B, T, n_kv, d]

@@ -23,6 +23,7 @@ import torch
 
 import sink_augmented_gqa_b200 as sa
 from oracle import int4 as oint4
+from sink_augmented_gqa_b200 import workloads as wl
 
 from helpers import check_lse, half_step, to64
 
@@ -172,3 +173,19 @@ def test_scores_rise_as_values_fall(cuda_device, n_q, n_kv, d, nats):
         k[:, g] = (t[:, None] * math.sqrt(d) / base.square().sum() * base).to(torch.bfloat16)
     v = (v.float() * torch.exp(-t)[:, None, None]).to(torch.bfloat16)
     _check(q, k, v, kn, vn, None, what="falling values")
+
+
+@pytest.mark.parametrize("over,n", [(dict(B=1, n_q=8, n_kv=1, d=64), 5000), (dict(B=30, n_q=16, n_kv=8, d=64), 700),
+                                    (dict(B=3, n_q=16, n_kv=2, d=128), 3000)])
+def test_identical_calls_give_identical_bits(cuda_device, over, n):
+    cfg = wl.scaled(wl.CONFIGS["tiny"], **over)
+    cache = sa.KVCache(cfg.B, (n + 16) // 16 * 16, cfg.n_kv, cfg.d, device=DEV, int4=True)
+    cache.append(*(t.to(DEV) for t in wl.prefilled_cache_rows(cfg, rows=n)))
+    q, k, v = (t.to(DEV) for t in wl.qkv(cfg, 1, step=1))
+    ws = sa.decode_workspace(cfg.B, cfg.n_q, cfg.n_kv, cfg.d, device=DEV)
+    snap, first = cache.snapshot(), None
+    for _ in range(20):
+        cache.restore(snap)
+        got = sa.attn_decode(cache, q, k, v, None, 0, cfg.sm_scale, rope_fused=False, workspace=ws, return_lse=True)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
