@@ -955,23 +955,26 @@ def run_reference(args, rank, world):
 
 PROFILE_CASES = ("handoff_prefill_full", "handoff_prefill_full_b4", "handoff_prefill_band", "handoff_decode_full_b4",
                  "gptoss_prefill_full", "gptoss_prefill_band", "lite_prefill_full", "long_decode_full",
-                 "long_decode_fp8", "gptoss_qkv_proj", "gptoss_out_proj", "lite_backward_b2")
+                 "long_decode_fp8", "gptoss_qkv_proj", "gptoss_out_proj", "lite_backward_b2", "handoff_decode_int4")
 
 
 def profile_case(name, dev, steps, warmup):
     import sink_augmented_gqa_b200 as sa
-    if name == "handoff_decode_full_b4":
+    if name in ("handoff_decode_full_b4", "handoff_decode_int4"):
         # a decode step of the handoff's full layer after the chunk (position
-        # 66,048: 66,049 rows read per sequence), for 4 of the 16 sequences
-        cfg = wl.scaled(wl.CONFIGS["handoff"], B=4)
-        off = cfg.offset + cfg.T
+        # 66,048: 66,049 rows read per sequence), for 4 of the 16 sequences;
+        # on an INT4 cache behind the 65,536 rows of all 16
+        int4 = name.endswith("int4")
+        cfg = wl.CONFIGS["handoff"] if int4 else wl.scaled(wl.CONFIGS["handoff"], B=4)
+        off = cfg.offset if int4 else cfg.offset + cfg.T
         y = cfg.yarn
         cos, sin = sa.yarn_rope_tables(off + 1, cfg.d, y["theta"], y["scaling"], y["orig_ctx"], y["alpha"],
                                        y["beta"], device=dev)
-        cache = sa.KVCache(cfg.B, off + 1, cfg.n_kv, cfg.d, device=dev)
+        cache = sa.KVCache(cfg.B, off + 16 if int4 else off + 1, cfg.n_kv, cfg.d, device=dev, int4=int4)
         kp, vp = wl.prefilled_cache_rows(cfg, layer=1, device=dev, rows=off)
         cache.append(kp, vp)
         del kp, vp
+        torch.cuda.empty_cache()
         snap = cache.snapshot()
         q, k, v = wl.qkv(cfg, 1, layer=1, step=1, device=dev)
         sinks = wl.sinks(cfg, 1, device=dev)
@@ -981,7 +984,7 @@ def profile_case(name, dev, steps, warmup):
         def once():
             cache.restore(snap)
             sa.attn_decode(cache, q, k, v, sinks, 0, cfg.sm_scale, cos, sin, workspace=ws, out=out)
-        units = cfg.B * (off + 1) * kv_row_bytes(cfg)
+        units = cfg.B * off * cfg.n_kv * (cfg.d + cfg.d // 8) if int4 else cfg.B * (off + 1) * kv_row_bytes(cfg)
         for _ in range(warmup + steps):
             once()
         torch.cuda.synchronize()

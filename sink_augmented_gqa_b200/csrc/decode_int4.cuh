@@ -1,9 +1,12 @@
 // One-token decode over an INT4 cache (int4.cuh). As in decode_kernel
 // (decode.cuh) a producer warp streams the rows through a ring of stages and
 // the consumer warps attend them, but with 4.5 bits an element the arithmetic
-// per byte is about four times that of a bf16 cache: the kernel is bound by
-// the ALU pipe (half the issue rate), so the codes go to the tensor cores with
-// as few instructions as possible, and every SM gets the same number of rows.
+// per byte is about four times that of a bf16 cache: of all units the issue
+// slots and the ALU pipe (half their rate) are the busiest, at about 60 % with
+// the four or five warps a scheduler has to hide latency with, and memory after
+// them. So the codes go to the tensor cores with as few instructions as
+// possible, and every SM gets the same number of rows. 16 sequences of 65,536
+// rows, 64 query and 8 KV heads of 64: 127 us back to back (4.7 TB/s).
 //
 // One CTA per SM, 16 consumer warps (d = 128: 12) that take 32 rows each of a
 // 512-row (384-row) stage (with two CTAs of 8 per SM the scheduler's older one
@@ -66,10 +69,11 @@ namespace sa {
 
 template <int D>
 struct DecodeI4Cfg {
-  // Consumer warps, 32 rows of a stage each. d = 128 holds 8 accumulators and 8
-  // fragment words a block of four blocks: 12 warps of 144 registers (16 sequences
-  // of 16,384 rows: 71.8 us) rather than 16 of 104, which spill (103). d = 64 the
-  // other way round: 16 sequences of 65,536 rows 137 us with 16 warps, 150 with 12.
+  // Consumer warps, 32 rows of a stage each. d = 128 holds 16 registers of sums and
+  // queries for each of four blocks: 12 warps of 144 registers (16 sequences of
+  // 16,384 rows, 64 / 8 heads: 71.8 us) rather than 16 of 104, which spill (103).
+  // d = 64 the other way round: 16 of 65,536 rows 138 us with 16 warps, 150 with
+  // 12. d = 96 has room in 104: 16 of 30,000 rows, 16 / 4 heads, 54.8 against 55.5.
   static constexpr int NCW = D == 128 ? 12 : 16;
   static constexpr int UNIT = 128;              // rows that shares count in
   static constexpr int R = 32 * NCW;            // rows per stage
