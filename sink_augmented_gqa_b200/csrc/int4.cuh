@@ -134,8 +134,9 @@ struct RowsCfg {
 
 // Appends T bf16 rows to an INT4 cache. Bound by reading them (4 d bytes a
 // position and KV head against 1.1 d written): 8 x 4,096 rows of 4 heads of 96
-// in 15.4 us back to back (50 MB read, 14 MB written: 4.2 TB/s; 1.3 waves of blocks),
-// 8,192 rows of 8 heads of 64 in a fused qkv in 5.5.
+// in 15.3 us back to back (50 MB read, 14 MB written: 4.2 TB/s; the last of this
+// grid's 1.3 waves of blocks is mostly empty), 8,192 rows of 8 heads of 64 in a fused
+// qkv in 5.6.
 template <int D, int NR>
 __global__ void __launch_bounds__(256) kv_append_i4_kernel(const RowsParams p) {
   using C = RowsCfg<D>;
@@ -234,7 +235,10 @@ __device__ __forceinline__ uint4 row8_bf16(const StoredRow8<KIND>& x) {
 
 // Reads T positions of a cache back as bf16 rows. Bound by writing them, which
 // DRAM takes at ~3.8 TB/s where little is read beside them: 131,071 rows of 8 heads
-// of 64 from INT4 in 68.3 us (268 MB written, 75 MB read).
+// of 64 from INT4 in 68.6 us (268 MB written, 75 MB read), from FP8 in 77.9, from bf16
+// in 93.8 (as many read as written: 5.7 TB/s). Where the rows written stay in L2 (25 MB:
+// 3 x 4,099 rows of 4 heads of 128 from FP8 in 9.3 us) it is a launch and one short
+// wave of loads.
 template <int D, int KIND, int NR>
 __global__ void __launch_bounds__(256) kv_read_kernel(const RowsParams p) {
   using C = RowsCfg<D>;

@@ -399,8 +399,8 @@ int prefill_tile_keys(int d) {
 // rows), two of them an item's start and end, parts adding a launch (~4 us)
 // and their partials' traffic. A whole call with and without this choice, d =
 // 64, behind 16,384 rows: 16 rows of 64 / 8 heads (8 heads a tile, 17 parts)
-// 29 us against 158; 128 rows (4 parts) 75 against 159; 900 rows of 4 / 4 heads
-// (9 parts) 45 against 206. Behind 600 rows, 60 rows of 16 / 2 heads: one head a
+// 28 us against 158; 128 rows (4 parts) 72 against 159; 900 rows of 4 / 4 heads
+// (9 parts) 44 against 206. Behind 600 rows, 60 rows of 16 / 2 heads: one head a
 // tile, no parts, 15.2; packed 19.1.
 struct PrefillSplit {
   int pack, tpos, splits;
@@ -408,8 +408,9 @@ struct PrefillSplit {
 };
 constexpr int kSplitTiles = 2;     // key tiles of a part, at least
 // Items of a split launch, at most: what the workspace holds, a little over two waves
-// of 148 SMs, so that items which half fill a second one can be cut finer (300 rows of 64 / 8 heads behind 16,384: 80 items of
-// 8 heads in 3 parts, 172 us, against 214 of 128 whole ones).
+// of 148 SMs, so that items which half fill a second one can be cut finer (300 rows
+// of 64 / 8 heads behind 16,384: 80 items of 8 heads in 3 parts, 168 us, against 214
+// of 128 whole ones).
 constexpr int kSplitSlots = 320;
 
 PrefillSplit plan_prefill(const sa_kv_cache* c, const sa_attn_args* a) {
@@ -666,7 +667,8 @@ struct DecodePlan {
 // two CTAs share, cost a CTA of an INT4 decode. d = 64, 8 KV heads, dealt out
 // against equal shares: 12 sequences of 5,500 rows (15 units more for the
 // fullest CTA) 16.6 us against 19.0; 7 of 16,000 (also 15) 24.4 against 23.6;
-// 12 of 8,000 (22) equal shares 23.
+// 12 of 8,000 (22) equal shares 23. (Before V's products had powers of two of
+// their own, which takes some 4 % more on either side.)
 constexpr long long kI4Border = 16;
 
 DecodePlan plan_decode(const sa_kv_cache* c, const sa_attn_args* a) {
